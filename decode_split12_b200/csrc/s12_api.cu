@@ -418,6 +418,37 @@ int s12_gemm_skinny_multi(const s12_view *views, int count, const uint16_t *cons
     return launch_gemm(views, count, x, M, yy, nullptr, ws, ws_bytes, err_flag, static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+// Checks shared by the norm and the quantiser, then the launch.
+int norm_call(const NormCall &c, void *stream) {
+    if (c.x_type != S12_TYPE_BF16 && c.x_type != S12_TYPE_F32) return S12_ERR_ARG;
+    if (c.residual_type != S12_TYPE_BF16 && c.residual_type != S12_TYPE_F32) return S12_ERR_ARG;
+    if (!(c.eps >= 0.f) || std::isinf(c.eps)) return S12_ERR_ARG;
+    if (c.rows < 0 || c.cols <= 0) return S12_ERR_ARG;
+    if (c.rows > 0x7FFFFFFFll || c.cols % 8 || c.cols > S12_NORM_MAX_COLS) return S12_ERR_SHAPE;
+    if (c.rows == 0) return S12_OK;
+    if (!c.x || (!c.y && !c.q) || (c.q && !c.scale)) return S12_ERR_ARG;
+    for (const void *p : {c.x, c.residual, static_cast<const void *>(c.residual_out),
+                          static_cast<const void *>(c.weight), static_cast<const void *>(c.y),
+                          static_cast<const void *>(c.q)})
+        if (!aligned16(p)) return S12_ERR_ALIGN;
+    if (!aligned4(c.scale)) return S12_ERR_ALIGN;
+    return launch_norm(c, static_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+int s12_rmsnorm(const void *x, int x_type, const void *residual, void *residual_out, int residual_type,
+                const uint16_t *weight, int64_t rows, int64_t cols, float eps, uint16_t *y, int8_t *q, float *scale,
+                void *stream) {
+    return norm_call({x, x_type, residual, residual_out, residual_type, weight, rows, cols, eps, true, y, q, scale},
+                     stream);
+}
+
+int s12_quant_i8(const void *x, int x_type, int64_t rows, int64_t cols, int8_t *q, float *scale, void *stream) {
+    return norm_call({x, x_type, nullptr, nullptr, S12_TYPE_BF16, nullptr, rows, cols, 0.f, false, nullptr, q, scale},
+                     stream);
+}
+
 size_t s12_stats_ws_bytes(void) { return 256 * sizeof(unsigned long long); }
 
 int s12_stats(const s12_view *v, s12_stats_t *out, void *ws, size_t ws_bytes, void *stream) {

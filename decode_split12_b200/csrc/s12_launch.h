@@ -74,4 +74,21 @@ size_t gemm_ws_bytes(const s12_view *views, int count, const int *M);
 int launch_gemm(const s12_view *views, int count, const uint16_t *const *x, const int *M, void *const *y,
                 const int *out, void *ws, size_t ws_bytes, uint32_t *err, cudaStream_t stream);
 
+// The RMS norm (normed) or the row quantiser (not normed: q and scale of x).
+struct NormCall {
+    const void *x;
+    int x_type;  // S12_TYPE_*
+    const void *residual;
+    void *residual_out;
+    int residual_type;
+    const uint16_t *weight;
+    int64_t rows, cols;
+    float eps;
+    bool normed;
+    uint16_t *y;
+    int8_t *q;
+    float *scale;
+};
+int launch_norm(const NormCall &c, cudaStream_t stream);
+
 }  // namespace s12

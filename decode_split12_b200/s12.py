@@ -41,8 +41,11 @@ EXPORTED = (
     "s12_gemm_skinny_multi", "s12_validate_host", "s12_plane_hashes_host", "s12_fnv1a64",
     "s12_to_v2_host", "s12_from_v2_host", "s12_to_v3_host", "s12_from_v3_host", "s12_load_bf16",
     "s12_stats_ws_bytes",
-    "s12_stats", "s12_bf16_gemv",
+    "s12_stats", "s12_bf16_gemv", "s12_rmsnorm", "s12_quant_i8",
 )
+
+S12_TYPE_BF16 = 0
+S12_TYPE_F32 = 1
 
 
 class S12Error(RuntimeError):
@@ -142,6 +145,10 @@ def _lib() -> C.CDLL:
         lib.s12_stats.restype = C.c_int
         lib.s12_bf16_gemv.argtypes = [_P, _I64, _I64, _P, C.c_int, _P, _P]
         lib.s12_bf16_gemv.restype = C.c_int
+        lib.s12_rmsnorm.argtypes = [_P, C.c_int, _P, _P, C.c_int, _P, _I64, _I64, C.c_float, _P, _P, _P, _P]
+        lib.s12_rmsnorm.restype = C.c_int
+        lib.s12_quant_i8.argtypes = [_P, C.c_int, _I64, _I64, _P, _P, _P]
+        lib.s12_quant_i8.restype = C.c_int
         _LIB = lib
     return _LIB
 
@@ -405,6 +412,97 @@ def s12_gemm_skinny_bf16(view: View, x: torch.Tensor, y: torch.Tensor | None = N
     _check(_lib().s12_gemm_skinny_bf16(C.byref(view), _dptr(x), M, _dptr(y), _dptr(ws), ws.numel(),
                                        _dptr(err_flag), _stream(stream)), "s12_gemm_skinny_bf16")
     return y
+
+
+def _on_current_device(*tensors):
+    """The library's pointers belong to the current device: refuse tensors
+    of another one (their addresses would be used there)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"expected tensors on the current device (cuda:{dev}), got {t.device}")
+
+
+def _value_type(t: torch.Tensor) -> int:
+    """S12_TYPE_* of a tensor: FP32, or BF16 (also as 16-bit patterns)."""
+    if t.dtype is torch.float32:
+        return S12_TYPE_F32
+    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        return S12_TYPE_BF16
+    raise TypeError(f"expected a BF16 (or 16-bit pattern) or FP32 tensor, got {t.dtype}")
+
+
+def _expect(t: torch.Tensor, shape, dtypes, name: str):
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {tuple(shape)} of {dtypes}, got {tuple(t.shape)} of {t.dtype}")
+
+
+_BITS16 = (torch.int16, torch.bfloat16, torch.uint16)
+
+
+def s12_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None, bf16: bool = True,
+                int8: bool = False, y: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                scale: torch.Tensor | None = None, stream=None):
+    """RMS norm of the last dimension of x (BF16 or FP32), after adding
+    `residual` to it; the sum goes to `residual_out`, which is the residual
+    itself where none is given.  Returns (y, q, scale, residual_out): y, the
+    norm as BF16 bits, where `bf16`; q (int8) and scale (FP32, one a row)
+    where `int8`; None for what was not asked for."""
+    if not (bf16 or int8):
+        raise ValueError("nothing to compute: neither bf16 nor int8")
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    if residual is not None:
+        _expect(residual, x.shape, (torch.float32,) + _BITS16, "residual")
+        if residual_out is None:
+            residual_out = residual
+    rt = S12_TYPE_BF16
+    if residual_out is not None:
+        rt = _value_type(residual_out)
+        _expect(residual_out, x.shape, (torch.float32,) + _BITS16, "residual_out")
+        if residual is not None and _value_type(residual) != rt:
+            raise ValueError("residual and residual_out must have the same type")
+    if weight is not None:
+        _expect(weight, (cols,), _BITS16, "weight")
+    if bf16:
+        if y is None:
+            y = torch.empty(x.shape, dtype=torch.int16, device=x.device)
+        else:
+            _expect(y, x.shape, _BITS16, "y")
+    if int8:
+        if q is None:
+            q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        else:
+            _expect(q, x.shape, (torch.int8,), "q")
+        if scale is None:
+            scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        else:
+            _expect(scale, x.shape[:-1], (torch.float32,), "scale")
+    y, q, scale = (y if bf16 else None), (q if int8 else None), (scale if int8 else None)
+    _on_current_device(x, weight, residual, residual_out, y, q, scale)
+    _check(_lib().s12_rmsnorm(_dptr(x), _value_type(x), _dptr(residual), _dptr(residual_out), rt, _dptr(weight), rows,
+                              cols, eps, _dptr(y), _dptr(q), _dptr(scale), _stream(stream)), "s12_rmsnorm")
+    return y, q, scale, residual_out
+
+
+def s12_quant_i8(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """(q, scale): the rows of x (BF16 or FP32, along its last dimension) as
+    int8 with one FP32 scale a row."""
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    else:
+        _expect(q, x.shape, (torch.int8,), "q")
+    if scale is None:
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    else:
+        _expect(scale, x.shape[:-1], (torch.float32,), "scale")
+    _on_current_device(x, q, scale)
+    _check(_lib().s12_quant_i8(_dptr(x), _value_type(x), rows, cols, _dptr(q), _dptr(scale), _stream(stream)),
+           "s12_quant_i8")
+    return q, scale
 
 
 def s12_stats(view: View, ws: torch.Tensor | None = None, stream=None) -> dict:

@@ -91,6 +91,11 @@ extern "C" {
 #define S12_GEMM_MIN_M 16
 #define S12_GEMM_MAX_M 256
 #define S12_GEMM_MAX_PROBLEMS 16 /* matrices per s12_gemm_skinny_multi call */
+#define S12_NORM_MAX_COLS 32768  /* longest row of s12_rmsnorm and s12_quant_i8 */
+
+/* ---- value types of the calls that take more than one ---- */
+#define S12_TYPE_BF16 0
+#define S12_TYPE_F32 1
 
 /* Host-side description of an opened container.  All pointers are device
  * pointers into the caller's container buffer.  A version 1 container has
@@ -374,6 +379,50 @@ size_t s12_gemm_multi_ws_bytes(const s12_view *views, int count, const int *M);
  * container versions. */
 int s12_gemm_skinny_multi(const s12_view *views, int count, const uint16_t *const *x, const int *M,
                           float *const *y, void *ws, size_t ws_bytes, uint32_t *err_flag, void *stream);
+
+/* ---- between the products: norm and 8-bit rows ---- */
+
+/* The pages have no counterpart of this call: a decoder stack needs it
+ * between the products.
+ * RMS norm of `rows` rows of `cols` values, with the residual's addition and
+ * a BF16 result, an 8-bit result with a scale per row, or both:
+ *   s = x + residual (FP32; s = x where residual is NULL),
+ *   residual_out = s rounded to residual_type (where it is not NULL),
+ *   v = s * weight / sqrt(mean of s^2 over the row + eps)   (FP32),
+ *   y = bf16_rne(v)                                (where y is not NULL),
+ *   scale = max |v| / 127, q = rint(v / scale)     (where q is not NULL).
+ * The norm is taken of the unrounded sum s.
+ *   x:        device, rows x cols row-major, x_type S12_TYPE_BF16 or
+ *             S12_TYPE_F32 (the outputs of s12_gemv_bf16 and s12_gemv).
+ *   residual: device or NULL, and residual_out: device or NULL, rows x cols
+ *             of residual_type.  They may be the same buffer (updated in
+ *             place); residual_out may also be x when their types agree.
+ *             Any other overlap of an output with an input is not allowed.
+ *             residual_out may be given without a residual (a copy of x).
+ *   weight:   device BF16, cols values, or NULL (all ones).
+ *   y:        device BF16, rows x cols.   q: device, rows x cols, with
+ *   scale:    device FP32, rows values (4-byte alignment; needed with q,
+ *             not written without it).  At least one of y and q is given.
+ * cols is a multiple of 8 up to S12_NORM_MAX_COLS (else S12_ERR_SHAPE), rows
+ * any number below 2^31; rows == 0 does nothing.  eps >= 0 and finite (else
+ * S12_ERR_ARG).
+ * A row of zeros has scale 0 and q 0.  A row with an infinity or a NaN (or
+ * one that s or s * weight overflows to) has q 0 and scale NaN, and y what
+ * FP32 arithmetic gives.  The sum of squares is held in FP32: it overflows,
+ * and the row's v become 0, for |s| above about 1e19.  q rounds an FP32
+ * quotient: a value within 2^-22 relative of a half step may go either way.
+ * The largest |q| of a finite row is 127, unless the row is all zeros. */
+int s12_rmsnorm(const void *x, int x_type, const void *residual, void *residual_out, int residual_type,
+                const uint16_t *weight, int64_t rows, int64_t cols, float eps, uint16_t *y, int8_t *q,
+                float *scale, void *stream);
+
+/* The pages have no counterpart of this call: it makes the 8-bit operands
+ * of s12_gemm_i8, from a weight matrix or from activations.
+ * Rows to 8 bits: scale[r] = max |x[r][.]| / 127, q = rint(x / scale), with
+ * the conventions and limits of s12_rmsnorm.
+ *   x: device, rows x cols, S12_TYPE_BF16 or S12_TYPE_F32.
+ *   q: device, rows x cols.   scale: device FP32, rows values. */
+int s12_quant_i8(const void *x, int x_type, int64_t rows, int64_t cols, int8_t *q, float *scale, void *stream);
 
 /* ---- statistics ([M] section 1: exponent entropy; [T] key points:
  * escape rate) ---- */
