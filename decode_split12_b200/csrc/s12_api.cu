@@ -419,6 +419,67 @@ int s12_gemm_skinny_multi(const s12_view *views, int count, const uint16_t *cons
 }
 
 namespace {
+// The shapes of a mixture-of-experts layer, before its pointers.
+int moe_shapes(const MoeCall &c) {
+    int rc = check_view(c.up);
+    if (rc == S12_OK) rc = check_view(c.down);
+    if (rc != S12_OK) return rc;
+    if (c.up->version != c.down->version || c.up->version > 2) return S12_ERR_ARG;
+    if (c.experts < 1 || c.experts > S12_MOE_MAX_EXPERTS || c.tokens < 0 || c.tokens > S12_MOE_MAX_TOKENS ||
+        c.top_k < 1 || c.top_k > S12_MOE_MAX_TOP_K)
+        return S12_ERR_SHAPE;
+    const uint64_t E = static_cast<uint64_t>(c.experts), H = c.up->cols, F = c.down->cols;
+    if (H > 0x3FFFFFFFull || F > 0x3FFFFFFFull || c.up->rows > 0x7FFFFFFFull || c.down->rows > 0x7FFFFFFFull)
+        return S12_ERR_SHAPE;
+    return c.up->rows == E * 2 * F && c.down->rows == E * H ? S12_OK : S12_ERR_SHAPE;
+}
+
+// The checks of both mixture-of-experts calls, then the launch.
+int moe_call(const MoeCall &c, void *ws, size_t ws_bytes, void *stream) {
+    const int rc = moe_shapes(c);
+    if (rc != S12_OK) return rc;
+    if (c.y_type != S12_TYPE_BF16 && c.y_type != S12_TYPE_F32) return S12_ERR_ARG;
+    if (c.tokens == 0) return S12_OK;
+    if (!c.x || !c.y || !ws) return S12_ERR_ARG;
+    if (!aligned16(c.x) || !aligned16(c.router) || !aligned16(ws)) return S12_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(c.y) & (c.y_type == S12_TYPE_F32 ? 3 : 1)) return S12_ERR_ALIGN;
+    if (!aligned4(c.ids) || !aligned4(c.weights) || !aligned4(c.ids_in) || !aligned4(c.weights_in) ||
+        !aligned4(c.err))
+        return S12_ERR_ALIGN;
+    return launch_moe(c, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+size_t s12_moe_ws_bytes(const s12_view *gate_up, const s12_view *down, int experts, int tokens, int top_k) {
+    MoeCall c = {};
+    c.up = gate_up;
+    c.down = down;
+    c.experts = experts;
+    c.tokens = tokens;
+    c.top_k = top_k;
+    return moe_shapes(c) == S12_OK ? moe_ws_bytes(c) : 0;
+}
+
+int s12_moe(const s12_view *gate_up, const s12_view *down, int experts, const uint16_t *x, int tokens,
+            const uint16_t *router, int top_k, int renorm, void *y, int y_type, int32_t *ids, float *weights, void *ws,
+            size_t ws_bytes, uint32_t *err_flag, void *stream) {
+    if (top_k > experts) return S12_ERR_SHAPE;
+    if (!router && tokens > 0) return S12_ERR_ARG;
+    return moe_call({gate_up, down, experts, x, tokens, router, nullptr, nullptr, top_k, renorm, y, y_type, ids, weights,
+                     err_flag},
+                    ws, ws_bytes, stream);
+}
+
+int s12_moe_routed(const s12_view *gate_up, const s12_view *down, int experts, const uint16_t *x, int tokens,
+                   const int32_t *ids, const float *weights, int top_k, void *y, int y_type, void *ws, size_t ws_bytes,
+                   uint32_t *err_flag, void *stream) {
+    if ((!ids || !weights) && tokens > 0) return S12_ERR_ARG;
+    return moe_call({gate_up, down, experts, x, tokens, nullptr, ids, weights, top_k, 0, y, y_type, nullptr, nullptr,
+                     err_flag},
+                    ws, ws_bytes, stream);
+}
+
+namespace {
 // Checks shared by the norm and the quantiser, then the launch.
 int norm_call(const NormCall &c, void *stream) {
     if (c.x_type != S12_TYPE_BF16 && c.x_type != S12_TYPE_F32) return S12_ERR_ARG;

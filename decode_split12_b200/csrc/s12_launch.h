@@ -91,4 +91,24 @@ struct NormCall {
 };
 int launch_norm(const NormCall &c, cudaStream_t stream);
 
+// The mixture-of-experts layer: routed by `router`, or by ids_in and
+// weights_in where ids_in is not null.
+struct MoeCall {
+    const s12_view *up, *down;
+    int experts;
+    const uint16_t *x;
+    int tokens;
+    const uint16_t *router;
+    const int32_t *ids_in;
+    const float *weights_in;
+    int top_k, renorm;
+    void *y;
+    int y_type;
+    int32_t *ids;
+    float *weights;
+    uint32_t *err;
+};
+size_t moe_ws_bytes(const MoeCall &c);
+int launch_moe(const MoeCall &c, void *ws, size_t ws_bytes, cudaStream_t stream);
+
 }  // namespace s12

@@ -42,6 +42,7 @@ EXPORTED = (
     "s12_to_v2_host", "s12_from_v2_host", "s12_to_v3_host", "s12_from_v3_host", "s12_load_bf16",
     "s12_stats_ws_bytes",
     "s12_stats", "s12_bf16_gemv", "s12_rmsnorm", "s12_quant_i8",
+    "s12_moe_ws_bytes", "s12_moe", "s12_moe_routed",
 )
 
 S12_TYPE_BF16 = 0
@@ -149,6 +150,14 @@ def _lib() -> C.CDLL:
         lib.s12_rmsnorm.restype = C.c_int
         lib.s12_quant_i8.argtypes = [_P, C.c_int, _I64, _I64, _P, _P, _P]
         lib.s12_quant_i8.restype = C.c_int
+        view = C.POINTER(View)
+        lib.s12_moe_ws_bytes.argtypes = [view, view, C.c_int, C.c_int, C.c_int]
+        lib.s12_moe_ws_bytes.restype = _SZ
+        lib.s12_moe.argtypes = [view, view, C.c_int, _P, C.c_int, _P, C.c_int, C.c_int, _P, C.c_int, _P, _P, _P, _SZ,
+                                _P, _P]
+        lib.s12_moe.restype = C.c_int
+        lib.s12_moe_routed.argtypes = [view, view, C.c_int, _P, C.c_int, _P, _P, C.c_int, _P, C.c_int, _P, _SZ, _P, _P]
+        lib.s12_moe_routed.restype = C.c_int
         _LIB = lib
     return _LIB
 
@@ -503,6 +512,77 @@ def s12_quant_i8(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Te
     _check(_lib().s12_quant_i8(_dptr(x), _value_type(x), rows, cols, _dptr(q), _dptr(scale), _stream(stream)),
            "s12_quant_i8")
     return q, scale
+
+
+def s12_moe_ws_bytes(gate_up: View, down: View, experts: int, tokens: int, top_k: int) -> int:
+    return int(_lib().s12_moe_ws_bytes(C.byref(gate_up), C.byref(down), experts, tokens, top_k))
+
+
+def moe_workspace(gate_up: View, down: View, experts: int, tokens: int, top_k: int, device=None) -> torch.Tensor:
+    """A zero-filled workspace for s12_moe and s12_moe_routed with these
+    containers and top_k, for up to `tokens` tokens."""
+    need = s12_moe_ws_bytes(gate_up, down, experts, tokens, top_k)
+    return torch.zeros(max(need, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def _moe_io(down: View, x: torch.Tensor, experts: int, y, f32: bool):
+    hidden = int(down.rows) // max(experts, 1)
+    if x.dim() != 2 or x.shape[1] != hidden or x.dtype not in _BITS16:
+        raise ValueError(f"x: expected (tokens, {hidden}) of 16-bit values, got {tuple(x.shape)} of {x.dtype}")
+    if y is None:
+        return torch.empty(x.shape, dtype=torch.float32 if f32 else torch.int16, device=x.device)
+    _expect(y, x.shape, (torch.float32,) + _BITS16, "y")
+    return y
+
+
+def s12_moe(gate_up: View, down: View, experts: int, x: torch.Tensor, router: torch.Tensor, top_k: int,
+            renorm: bool = True, y: torch.Tensor | None = None, ids: torch.Tensor | None = None,
+            weights: torch.Tensor | None = None, ws: torch.Tensor | None = None, err_flag: torch.Tensor | None = None,
+            stream=None, f32: bool = False):
+    """A whole mixture-of-experts layer: (y, ids, weights), y as BF16 bits (or
+    FP32 where `f32`, or in the type of the y that is given), the chosen
+    experts (int32) and their weights (FP32), tokens x top_k.  gate_up is the
+    container of interleave_gate_up(gate, up) of the experts' matrices
+    stacked along their rows, down that of the stacked down matrices."""
+    y = _moe_io(down, x, experts, y, f32)
+    T = x.shape[0]
+    _expect(router, (experts, x.shape[1]), _BITS16, "router")
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+    else:
+        _expect(ids, (T, top_k), (torch.int32,), "ids")
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+    else:
+        _expect(weights, (T, top_k), (torch.float32,), "weights")
+    if ws is None:
+        ws = moe_workspace(gate_up, down, experts, T, top_k, x.device)
+    _on_current_device(x, router, y, ids, weights, ws, err_flag)
+    _check(_lib().s12_moe(C.byref(gate_up), C.byref(down), experts, _dptr(x), T, _dptr(router), top_k, int(renorm),
+                          _dptr(y), _value_type(y), _dptr(ids), _dptr(weights), _dptr(ws), ws.numel(),
+                          _dptr(err_flag), _stream(stream)), "s12_moe")
+    return y, ids, weights
+
+
+def s12_moe_routed(gate_up: View, down: View, experts: int, x: torch.Tensor, ids: torch.Tensor,
+                   weights: torch.Tensor, y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                   err_flag: torch.Tensor | None = None, stream=None, f32: bool = False) -> torch.Tensor:
+    """s12_moe with the routing given (ids int32 and weights FP32, tokens x
+    top_k; an id outside [0, experts) leaves its slot out): y."""
+    y = _moe_io(down, x, experts, y, f32)
+    T = x.shape[0]
+    if ids.dim() != 2:
+        raise ValueError("ids must be tokens x top_k")
+    _expect(ids, (T, ids.shape[1]), (torch.int32,), "ids")
+    _expect(weights, tuple(ids.shape), (torch.float32,), "weights")
+    top_k = ids.shape[1]
+    if ws is None:
+        ws = moe_workspace(gate_up, down, experts, T, top_k, x.device)
+    _on_current_device(x, ids, weights, y, ws, err_flag)
+    _check(_lib().s12_moe_routed(C.byref(gate_up), C.byref(down), experts, _dptr(x), T, _dptr(ids), _dptr(weights),
+                                 top_k, _dptr(y), _value_type(y), _dptr(ws), ws.numel(), _dptr(err_flag),
+                                 _stream(stream)), "s12_moe_routed")
+    return y
 
 
 def s12_stats(view: View, ws: torch.Tensor | None = None, stream=None) -> dict:

@@ -92,6 +92,9 @@ extern "C" {
 #define S12_GEMM_MAX_M 256
 #define S12_GEMM_MAX_PROBLEMS 16 /* matrices per s12_gemm_skinny_multi call */
 #define S12_NORM_MAX_COLS 32768  /* longest row of s12_rmsnorm and s12_quant_i8 */
+#define S12_MOE_MAX_TOKENS 64   /* tokens of one s12_moe call */
+#define S12_MOE_MAX_TOP_K 8     /* experts a token is sent to */
+#define S12_MOE_MAX_EXPERTS 256
 
 /* ---- value types of the calls that take more than one ---- */
 #define S12_TYPE_BF16 0
@@ -379,6 +382,72 @@ size_t s12_gemm_multi_ws_bytes(const s12_view *views, int count, const int *M);
  * container versions. */
 int s12_gemm_skinny_multi(const s12_view *views, int count, const uint16_t *const *x, const int *M,
                           float *const *y, void *ws, size_t ws_bytes, uint32_t *err_flag, void *stream);
+
+/* ---- mixture-of-experts layer ---- */
+
+/* Workspace bytes s12_moe and s12_moe_routed need for these containers (0
+ * for invalid arguments).  The size grows with each of tokens, top_k and
+ * experts, so one sized for the largest call serves smaller ones of the
+ * same containers. */
+size_t s12_moe_ws_bytes(const s12_view *gate_up, const s12_view *down, int experts, int tokens, int top_k);
+
+/* Follows: [W] "What does 'lossless' mean for LLM weights?" (decode into
+ * registers and multiply at once); the layer around the products is this
+ * library's own.
+ * A whole mixture-of-experts layer for a few tokens, in one kernel:
+ *   score[t][e] = sum_k router[e][k] * x[t][k],
+ *   the top_k experts of each token by score (the lower index first where
+ *   two are equal), with weights softmax(score): over all experts, or over
+ *   the chosen ones where renorm is not 0,
+ *   y[t] = sum over the slots s, e = ids[t][s], of
+ *          weights[t][s] * W_down_e (silu(W_gate_e x_t) * (W_up_e x_t)).
+ *   gate_up: ONE container of experts * 2F rows and H columns: expert after
+ *            expert, each with gate and up interleaved in blocks of 8 rows
+ *            as in s12_gemv_swiglu (the binding's interleave_gate_up, applied
+ *            to the stacked matrices, builds it).
+ *   down:    ONE container of experts * H rows and F columns.  Shapes that do
+ *            not fit together give S12_ERR_SHAPE.  Both are version 1, or
+ *            both version 2.
+ *   x:       device BF16, tokens x H; 0 <= tokens <= S12_MOE_MAX_TOKENS (0
+ *            does nothing).
+ *   router:  device BF16, experts x H; 1 <= experts <= S12_MOE_MAX_EXPERTS,
+ *            1 <= top_k <= min(experts, S12_MOE_MAX_TOP_K).
+ *   y:       device, tokens x H, y_type S12_TYPE_BF16 (2-byte alignment) or
+ *            S12_TYPE_F32 (4-byte), overwritten.  It must not overlap an
+ *            input.
+ *   ids, weights: device int32 and FP32, tokens x top_k, or NULL: the chosen
+ *            experts, largest score first, and their weights.
+ *   ws:      device workspace of s12_moe_ws_bytes bytes (else
+ *            S12_ERR_CAPACITY), ZERO-FILLED before its first use and usable
+ *            again by any later call with containers and experts of the same
+ *            shapes (another layer's, say) for which it is large enough,
+ *            captured in a graph or not.  Calls of other shapes place its
+ *            parts elsewhere: they need a workspace of their own, or a zero
+ *            fill between.  Calls that may run at the same time need
+ *            different workspaces.
+ * The scores are sums in 64 bits.  The products accumulate in FP32 and the
+ * hidden values are held as the sum of two BF16 values, so y is within 1e-3
+ * of the sum of its terms' magnitudes before its own rounding, as in
+ * s12_gemv; repeated calls give identical y.  A token with a NaN score gets
+ * NaN weights and a NaN y; other tokens are not affected.
+ * With err_flag given, the escape counts of tile rows with escapes are
+ * checked against their spans and bases above 241 are flagged.
+ * The kernel is a cooperative launch of one block per SM that meets twice; a
+ * bounded wait that gives up sets S12_FLAG_TIMEOUT (y is then not valid) and
+ * leaves the workspace ready for the next call. */
+int s12_moe(const s12_view *gate_up, const s12_view *down, int experts, const uint16_t *x, int tokens,
+            const uint16_t *router, int top_k, int renorm, void *y, int y_type, int32_t *ids, float *weights,
+            void *ws, size_t ws_bytes, uint32_t *err_flag, void *stream);
+
+/* Follows: as s12_moe ([W] "What does 'lossless' mean for LLM weights?").
+ * s12_moe with the routing given: ids (device int32, tokens x top_k) and
+ * weights (device FP32, tokens x top_k).  A slot whose id is outside
+ * [0, experts) is left out, whatever its weight; a token with no slot left
+ * gets y = 0.  An id may appear more than once in a token.  1 <= top_k <=
+ * S12_MOE_MAX_TOP_K (it may exceed experts here). */
+int s12_moe_routed(const s12_view *gate_up, const s12_view *down, int experts, const uint16_t *x, int tokens,
+                   const int32_t *ids, const float *weights, int top_k, void *y, int y_type, void *ws,
+                   size_t ws_bytes, uint32_t *err_flag, void *stream);
 
 /* ---- between the products: norm and 8-bit rows ---- */
 

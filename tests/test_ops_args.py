@@ -54,3 +54,54 @@ def test_quant_refusals(s12):
     assert quant(cols=20) == S and quant(cols=32776) == S and quant(rows=1 << 31) == S
     assert quant(x=ODD) == L and quant(q=ODD) == L and quant(scale=ODD) == L
     assert quant(rows=0, x=None, q=None, scale=None) == s12.S12_OK
+
+
+def views(s12, E=4, H=256, F=128, version=1):
+    out = []
+    for rows, cols in ((E * 2 * F, H), (E * H, F)):
+        v = s12.View()
+        v.rows, v.cols, v.n_tiles, v.version = rows, cols, rows * cols // 128, version
+        for f in ("container", "raw", "code", "base", "esc_off", "esc", "tmeta", "row_esc"):
+            setattr(v, f, 0x100000)
+        out.append(v)
+    return out
+
+
+def test_moe_refusals(s12):
+    lib = s12.lib()
+    A, S, L = s12.S12_ERR_ARG, s12.S12_ERR_SHAPE, s12.S12_ERR_ALIGN
+
+    def moe(up=None, down=None, E=4, x=OK_PTR, T=3, router=OK_PTR, k=2, y=OK_PTR, yt=0, ids=None, w=None, ws=OK_PTR,
+            n=1 << 40, err=None):
+        u, d = views(s12)
+        return lib.s12_moe(C.byref(up or u), C.byref(down or d), E, x, T, router, k, 1, y, yt, ids, w, ws, n, err, None)
+
+    def routed(E=4, x=OK_PTR, T=3, ids=OK_PTR, w=OK_PTR, k=2, y=OK_PTR, yt=0, ws=OK_PTR, n=1 << 40):
+        u, d = views(s12)
+        return lib.s12_moe_routed(C.byref(u), C.byref(d), E, x, T, ids, w, k, y, yt, ws, n, None, None)
+
+    for call in (moe, routed):
+        assert call(x=None) == A and call(y=None) == A and call(ws=None) == A and call(yt=7) == A
+        assert call(E=3) == S and call(E=0) == S and call(E=-1) == S and call(E=257) == S
+        assert call(T=-1) == S and call(T=65) == S
+        assert call(k=0) == S and call(k=9) == S
+        assert call(x=FOUR) == L and call(ws=FOUR) == L and call(y=ODD) == L and call(y=C.c_void_p(0x100002), yt=1) == L
+        assert call(T=0, x=None, y=None, ws=None) == s12.S12_OK
+    assert moe(k=5) == S  # more than experts
+    assert moe(router=None) == A and moe(router=FOUR) == L
+    assert moe(ids=ODD) == L and moe(w=ODD) == L and moe(err=ODD) == L
+    assert routed(ids=None) == A and routed(w=None) == A and routed(ids=ODD) == L and routed(w=ODD) == L
+    # containers: versions that differ, or that the products do not read; shapes that do not belong together
+    u2, d2 = views(s12, version=2)
+    assert moe(up=u2) == A and moe(down=d2) == A
+    u3, d3 = views(s12, version=3)
+    assert moe(up=u3, down=d3) == A
+    u, d = views(s12)
+    assert moe(up=d, down=u) == S
+    u.rows += 16
+    assert moe(up=u) == S
+    assert moe(up=s12.View()) == A
+    assert lib.s12_moe_ws_bytes(C.byref(u), C.byref(d), 4, 3, 2) == 0
+    u, d = views(s12)
+    assert lib.s12_moe_ws_bytes(C.byref(u), C.byref(d), 4, 65, 2) == 0
+    assert lib.s12_moe_ws_bytes(C.byref(u), C.byref(d), 4, 3, 9) == 0
