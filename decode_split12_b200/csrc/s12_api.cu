@@ -479,6 +479,22 @@ int s12_moe_routed(const s12_view *gate_up, const s12_view *down, int experts, c
                     ws, ws_bytes, stream);
 }
 
+size_t s12_gemm_i8_ws_bytes(int64_t M) { return M < 0 || M > 0x7FFFFFFFll ? 0 : gemm_i8_ws_bytes(M > 0 ? M : 1); }
+
+int s12_gemm_i8(const int8_t *x, const float *x_scale, const int8_t *w, const float *w_scale, int64_t M, int64_t N,
+                int64_t K, void *y, int y_type, void *ws, size_t ws_bytes, uint32_t *err_flag, void *stream) {
+    if (y_type != S12_TYPE_BF16 && y_type != S12_TYPE_F32) return S12_ERR_ARG;
+    if (M < 0 || N < 0 || M > 0x7FFFFFFFll || N > 0x7FFFFFFFll) return S12_ERR_SHAPE;
+    if (K <= 0 || K % 16 || K > S12_GEMM_I8_MAX_K) return S12_ERR_SHAPE;
+    if (M == 0 || N == 0) return S12_OK;
+    if (!x || !x_scale || !w || !w_scale || !y || !ws) return S12_ERR_ARG;
+    if (!aligned16(x) || !aligned16(w) || !aligned16(ws)) return S12_ERR_ALIGN;
+    if (!aligned4(x_scale) || !aligned4(w_scale) || !aligned4(err_flag)) return S12_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(y) & (y_type == S12_TYPE_F32 ? 3 : 1)) return S12_ERR_ALIGN;
+    return launch_gemm_i8({x, w, x_scale, w_scale, M, N, K, y, y_type, err_flag}, ws, ws_bytes,
+                          static_cast<cudaStream_t>(stream));
+}
+
 namespace {
 // Checks shared by the norm and the quantiser, then the launch.
 int norm_call(const NormCall &c, void *stream) {

@@ -91,6 +91,18 @@ struct NormCall {
 };
 int launch_norm(const NormCall &c, cudaStream_t stream);
 
+// The 8-bit product y = x_scale * w_scale * (x w^T).
+struct Gemm8Call {
+    const int8_t *x, *w;
+    const float *x_scale, *w_scale;
+    int64_t M, N, K;
+    void *y;
+    int y_type;
+    uint32_t *err;
+};
+size_t gemm_i8_ws_bytes(int64_t M);
+int launch_gemm_i8(const Gemm8Call &c, void *ws, size_t ws_bytes, cudaStream_t stream);
+
 // The mixture-of-experts layer: routed by `router`, or by ids_in and
 // weights_in where ids_in is not null.
 struct MoeCall {

@@ -42,7 +42,7 @@ EXPORTED = (
     "s12_to_v2_host", "s12_from_v2_host", "s12_to_v3_host", "s12_from_v3_host", "s12_load_bf16",
     "s12_stats_ws_bytes",
     "s12_stats", "s12_bf16_gemv", "s12_rmsnorm", "s12_quant_i8",
-    "s12_moe_ws_bytes", "s12_moe", "s12_moe_routed",
+    "s12_moe_ws_bytes", "s12_moe", "s12_moe_routed", "s12_gemm_i8_ws_bytes", "s12_gemm_i8",
 )
 
 S12_TYPE_BF16 = 0
@@ -150,6 +150,10 @@ def _lib() -> C.CDLL:
         lib.s12_rmsnorm.restype = C.c_int
         lib.s12_quant_i8.argtypes = [_P, C.c_int, _I64, _I64, _P, _P, _P]
         lib.s12_quant_i8.restype = C.c_int
+        lib.s12_gemm_i8_ws_bytes.argtypes = [_I64]
+        lib.s12_gemm_i8_ws_bytes.restype = _SZ
+        lib.s12_gemm_i8.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _P, C.c_int, _P, _SZ, _P, _P]
+        lib.s12_gemm_i8.restype = C.c_int
         view = C.POINTER(View)
         lib.s12_moe_ws_bytes.argtypes = [view, view, C.c_int, C.c_int, C.c_int]
         lib.s12_moe_ws_bytes.restype = _SZ
@@ -512,6 +516,39 @@ def s12_quant_i8(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Te
     _check(_lib().s12_quant_i8(_dptr(x), _value_type(x), rows, cols, _dptr(q), _dptr(scale), _stream(stream)),
            "s12_quant_i8")
     return q, scale
+
+
+def s12_gemm_i8_ws_bytes(M: int) -> int:
+    return int(_lib().s12_gemm_i8_ws_bytes(M))
+
+
+def gemm_i8_workspace(M: int, N: int = 0, K: int = 0, device=None) -> torch.Tensor:
+    """A zero-filled workspace for s12_gemm_i8 with M tokens (its size does
+    not depend on N and K)."""
+    return torch.zeros(max(s12_gemm_i8_ws_bytes(M), 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def s12_gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                y: torch.Tensor | None = None, ws: torch.Tensor | None = None, err_flag: torch.Tensor | None = None,
+                stream=None, f32: bool = False) -> torch.Tensor:
+    """y = x_scale[m] * w_scale[n] * (x w^T) of int8 x (M, K) and w (N, K), as
+    BF16 bits (or FP32 where `f32`, or in the type of the y that is given)."""
+    M, K = x.shape
+    N = w.shape[0]
+    _expect(x, (M, K), (torch.int8,), "x")
+    _expect(w, (N, K), (torch.int8,), "w")
+    _expect(x_scale, (M,), (torch.float32,), "x_scale")
+    _expect(w_scale, (N,), (torch.float32,), "w_scale")
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.float32 if f32 else torch.int16, device=x.device)
+    else:
+        _expect(y, (M, N), (torch.float32,) + _BITS16, "y")
+    if ws is None:
+        ws = gemm_i8_workspace(M, device=x.device)
+    _on_current_device(x, x_scale, w, w_scale, y, ws, err_flag)
+    _check(_lib().s12_gemm_i8(_dptr(x), _dptr(x_scale), _dptr(w), _dptr(w_scale), M, N, K, _dptr(y), _value_type(y),
+                              _dptr(ws), ws.numel(), _dptr(err_flag), _stream(stream)), "s12_gemm_i8")
+    return y
 
 
 def s12_moe_ws_bytes(gate_up: View, down: View, experts: int, tokens: int, top_k: int) -> int:

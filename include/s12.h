@@ -92,6 +92,7 @@ extern "C" {
 #define S12_GEMM_MAX_M 256
 #define S12_GEMM_MAX_PROBLEMS 16 /* matrices per s12_gemm_skinny_multi call */
 #define S12_NORM_MAX_COLS 32768  /* longest row of s12_rmsnorm and s12_quant_i8 */
+#define S12_GEMM_I8_MAX_K 131056 /* columns of s12_gemm_i8: its int32 sums are exact */
 #define S12_MOE_MAX_TOKENS 64   /* tokens of one s12_moe call */
 #define S12_MOE_MAX_TOP_K 8     /* experts a token is sent to */
 #define S12_MOE_MAX_EXPERTS 256
@@ -492,6 +493,37 @@ int s12_rmsnorm(const void *x, int x_type, const void *residual, void *residual_
  *   x: device, rows x cols, S12_TYPE_BF16 or S12_TYPE_F32.
  *   q: device, rows x cols.   scale: device FP32, rows values. */
 int s12_quant_i8(const void *x, int x_type, int64_t rows, int64_t cols, int8_t *q, float *scale, void *stream);
+
+/* ---- 8-bit product ---- */
+
+/* Workspace bytes s12_gemm_i8 needs for M tokens (0 for M < 0 or above
+ * 2^31 - 1; the size does not depend on N and K, and one for the M that
+ * needs most serves every call on that device: any M >= 241 needs at most
+ * what M = 256 does). */
+size_t s12_gemm_i8_ws_bytes(int64_t M);
+
+/* Follows: [W] opening comparison of lossless weights with 8-bit ones (Q8_0):
+ * the 8-bit product that the lossless one is compared with; its scales per
+ * token and output channel, and the kernel, are this library's own.
+ * y[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] * w[n][k], on the tensor
+ * cores with exact int32 sums.
+ *   x: device int8, M x K row-major, x_scale: device FP32, M values (of
+ *      s12_quant_i8 or s12_rmsnorm).
+ *   w: device int8, N x K row-major, w_scale: device FP32, N values.
+ *   y: device, M x N row-major, y_type S12_TYPE_BF16 (2-byte alignment) or
+ *      S12_TYPE_F32 (4-byte), overwritten.
+ *   ws: device workspace of s12_gemm_i8_ws_bytes(M) bytes (else
+ *      S12_ERR_CAPACITY), ZERO-FILLED before its first use; calls of any
+ *      shapes for which it is large enough may use it one after the other.
+ *      Calls that may run at the same time need different workspaces.
+ * K is a multiple of 16 up to S12_GEMM_I8_MAX_K; 0 <= M, N < 2^31 (M == 0 or
+ * N == 0 does nothing); else S12_ERR_SHAPE.  All values of int8 are allowed.
+ * The scales multiply the sum in FP32, x_scale first, and y is rounded once;
+ * repeated calls give identical y.  A scale that is NaN (a row that was not
+ * finite) makes its row or column of y NaN.  err_flag (nullable) receives
+ * S12_FLAG_TIMEOUT when a bounded wait gave up (y is then not valid). */
+int s12_gemm_i8(const int8_t *x, const float *x_scale, const int8_t *w, const float *w_scale, int64_t M, int64_t N,
+                int64_t K, void *y, int y_type, void *ws, size_t ws_bytes, uint32_t *err_flag, void *stream);
 
 /* ---- statistics ([M] section 1: exponent entropy; [T] key points:
  * escape rate) ---- */

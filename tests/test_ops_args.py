@@ -105,3 +105,24 @@ def test_moe_refusals(s12):
     u, d = views(s12)
     assert lib.s12_moe_ws_bytes(C.byref(u), C.byref(d), 4, 65, 2) == 0
     assert lib.s12_moe_ws_bytes(C.byref(u), C.byref(d), 4, 3, 9) == 0
+
+
+def test_gemm_i8_refusals(s12):
+    lib = s12.lib()
+    A, S, L = s12.S12_ERR_ARG, s12.S12_ERR_SHAPE, s12.S12_ERR_ALIGN
+
+    def call(x=OK_PTR, sx=OK_PTR, w=OK_PTR, sw=OK_PTR, M=3, N=40, K=64, y=OK_PTR, yt=0, ws=OK_PTR, n=1 << 40, err=None):
+        return lib.s12_gemm_i8(x, sx, w, sw, M, N, K, y, yt, ws, n, err, None)
+
+    for name in ("x", "sx", "w", "sw", "y", "ws"):
+        assert call(**{name: None}) == A
+    assert call(yt=2) == A
+    assert call(M=-1) == S and call(N=-1) == S and call(M=1 << 31) == S and call(N=1 << 31) == S
+    for K in (0, -16, 8, 24, 131072, 1 << 40):
+        assert call(K=K) == S
+    for name in ("x", "w", "ws"):
+        assert call(**{name: FOUR}) == L
+    assert call(sx=ODD) == L and call(sw=ODD) == L and call(y=ODD) == L and call(err=ODD) == L
+    assert call(y=C.c_void_p(0x100002), yt=1) == L
+    assert call(M=0, x=None, y=None) == s12.S12_OK and call(N=0, w=None, ws=None) == s12.S12_OK
+    assert lib.s12_gemm_i8_ws_bytes(-1) == 0 and lib.s12_gemm_i8_ws_bytes(1 << 31) == 0
