@@ -4,10 +4,10 @@
 //   y[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] * w[n][k]
 //
 // x: M x K int8, w: N x K int8, sums in int32 (exact for K < 2^17), y BF16 or
-// FP32, rounded once.  Computed as Y^T = W * X^T, as the fused GEMM: 128 rows
-// of W are the tensor core's M and up to 256 tokens its N, so one kernel
-// serves a single token (N = 16: bound by reading W) and prompts (bound by
-// the tensor cores).
+// FP32, rounded once.  Computed as Y^T = W * X^T, as the fused GEMM: rows of W
+// are the tensor core's M and up to 256 tokens its N, so one kernel serves a
+// single token (N = 16: bound by reading W) and prompts (bound by the tensor
+// cores).
 //
 // One CTA per SM, six warps with fixed roles: a TMA producer (128 columns of W
 // and X a stage, 128-byte swizzle), the MMA issuer (four tcgen05.mma.kind::i8
@@ -15,11 +15,18 @@
 // TMEM, scale and store them.  There are two accumulators, so that the next
 // tile is multiplied while one is stored.
 //
-// Work split.  As many whole waves of tiles as there are go one tile to a CTA,
-// neighbours at the same time (they share rows of W or X in L2); the columns
-// of the tiles that are left are dealt to all CTAs in equal ranges.  A tile
-// that several CTAs share is finished by the last of them to arrive, which
-// adds the parts.  Integer sums do not depend on their order.
+// CG = 1: a CTA multiplies 128 rows of W.  CG = 2 (more than 128 tokens): two
+// CTAs share one product of 256 rows and up to 256 tokens (cta_group::2).  Each
+// loads its own rows of W and half of the tokens, 32 KB a stage instead of 48:
+// at 128 x 256 x 128 the tensor cores take a stage faster than L2 delivers 48.
+//
+// Work split.  The tiles that fill no whole wave of the grid come first: their
+// stages are dealt to the CTAs in equal ranges, at most kShare ranges a tile.
+// The whole waves follow, one tile to a CTA, neighbours at the same time (they
+// share rows of W or X in L2), and hide the joining of the shared tiles.  A
+// CTA that holds a part of a tile writes its sums to the workspace; the last
+// to arrive adds the others' to its own, scales and stores.  Integer sums do
+// not depend on their order.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -38,12 +45,13 @@ constexpr int kChunk = 128;   // columns per stage: one swizzle atom
 constexpr int kMaxTokens = 256;
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 4;
+constexpr int kShare = 8;     // ranges that a shared tile is cut into at most
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr uint32_t kWBytes = kRows * kChunk;
 
 struct __align__(64) Params {
     CUtensorMap tm_w;  // u8 [N][K], box 128 x 128, 128-byte swizzle, zeros past the ends
-    CUtensorMap tm_x;  // u8 [M][K], box 128 x tokens
+    CUtensorMap tm_x;  // u8 [M][K], box 128 x tokens / CG
     const float *x_scale, *w_scale;
     void *y;
     int y_f32;
@@ -51,89 +59,178 @@ struct __align__(64) Params {
     int tokens;              // per tile, a multiple of 16
     int chunks;              // stages per tile
     int tiles_m, waves;      // token tiles; whole waves of tiles
-    long long tile0, units;  // first tile after the whole waves, and the stages from there on
-    uint32_t *cnt;           // workspace: one arrival counter per CTA (zero between calls)
+    int rest, ranges;        // tiles before them, and the workers (from 0) that their stages are dealt to
+    long long units;         // those tiles' stages
     uint32_t *err;
-    int32_t *part;           // workspace: [CTAs][2][tokens][kRows] parts
+    uint32_t *cnt;           // workspace: one arrival counter per CTA (zero between calls)
+    int32_t *part;           // workspace: [CTAs][2][tokens][kRows] parts of shared tiles
     int stages;
-    uint32_t stage_bytes, acc_cols, tmem_cols;
+    uint32_t stage_bytes, acc_cols, tmem_cols;  // of one CTA
 };
 
-// D[tmem] (+)= A[smem] * B[smem] for one 128 x N x 32 step, int8 -> int32.
+// D[tmem] (+)= A[smem] * B[smem] for one (128 CG) x N x 32 step, int8 -> int32.
+template <int CG>
 __device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                         uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
 
 // Instruction descriptor: int8 x int8 -> int32, both operands K-major, M =
-// 128, N = n.
+// 128 CG, N = n.
+template <int CG>
 __device__ __forceinline__ uint32_t instr_desc(int n) {
     return (2u << 4)                                  // D format int32
            | (1u << 7)                                // A format signed
            | (1u << 10)                               // B format signed
            | (static_cast<uint32_t>(n >> 3) << 17)    // N / 8
-           | (static_cast<uint32_t>(kRows >> 4) << 24);  // M / 16
+           | (static_cast<uint32_t>(CG * kRows >> 4) << 24);  // M / 16
 }
 
-// The stretches of work of one CTA, in order: whole tiles, then its range of
-// the rest.  [k0, k1): the stages of the tile.
+// The pair's other half.  An address of this CTA's shared memory as the
+// leader's (rank 0) address of the same place.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t a) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Arrive on a barrier of the leader.
+__device__ __forceinline__ void arrive_at_leader(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
+}
+
+// Bounded wait for a phase that the other CTA takes part in.
+__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity) {
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (clock64() - t0 > kWaitCycles) return false;
+    }
+}
+
+// TMA copy into this CTA that completes on the leader's barrier.
+__device__ __forceinline__ void tma2d_pair(uint32_t dst, const CUtensorMap *tm, int c0, int c1, uint32_t leader_bar,
+                                           uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(tm), "r"(c0), "r"(c1), "r"(leader_bar), "l"(policy)
+        : "memory");
+}
+
+// Arrive on `bar` of both CTAs once every product that this thread issued so
+// far has completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (CG == 1)
+        umma_commit(bar);
+    else
+        commit_pair(bar);
+}
+
+// The stretches of work of one worker (a CTA or a pair), in order: its range of
+// the first tiles, then whole ones.  [k0, k1): the stages of the tile.
 struct Work {
     long long tile;
     int k0, k1;
+
+    __device__ __forceinline__ bool whole(const Params &p) const { return k0 == 0 && k1 == p.chunks; }
 };
 
-__device__ __forceinline__ long long range_start(const Params &p, long long c) { return c * p.units / gridDim.x; }
+// First stage of worker c's range.
+__device__ __forceinline__ long long range_start(const Params &p, int c) {
+    return c < p.ranges ? c * p.units / p.ranges : p.units;
+}
 
+template <int CG>
 struct Walk {
     int wave;
-    long long u, u1;  // position in the rest
+    long long u, u1;  // position in the first tiles
 
     __device__ __forceinline__ explicit Walk(const Params &p)
-        : wave(0), u(range_start(p, blockIdx.x)), u1(range_start(p, blockIdx.x + 1)) {}
+        : wave(0), u(range_start(p, blockIdx.x / CG)), u1(range_start(p, blockIdx.x / CG + 1)) {}
 
     __device__ __forceinline__ bool next(const Params &p, Work &w) {
-        if (wave < p.waves) {
-            w.tile = static_cast<long long>(wave) * gridDim.x + blockIdx.x;
-            w.k0 = 0;
-            w.k1 = p.chunks;
-            ++wave;
+        if (u < u1) {
+            w.tile = u / p.chunks;
+            const long long t0 = w.tile * p.chunks;
+            w.k0 = static_cast<int>(u - t0);
+            w.k1 = static_cast<int>(min(static_cast<long long>(p.chunks), u1 - t0));
+            u = t0 + w.k1;
             return true;
         }
-        if (u >= u1) return false;
-        const long long t = u / p.chunks, t0 = t * p.chunks;
-        w.tile = p.tile0 + t;
-        w.k0 = static_cast<int>(u - t0);
-        w.k1 = static_cast<int>(min(static_cast<long long>(p.chunks), u1 - t0));
-        u = t0 + w.k1;
+        if (wave == p.waves) return false;
+        w.tile = p.rest + static_cast<long long>(wave) * (gridDim.x / CG) + blockIdx.x / CG;
+        w.k0 = 0;
+        w.k1 = p.chunks;
+        ++wave;
         return true;
     }
 };
 
-// CTAs [first, last] that share tile t of the rest.
+// The workers [first, last] that share tile t (there are no more ranges than
+// stages, so every one of them holds some).  The first one's counter is the
+// tile's: a worker is the first of one shared tile at most.
 __device__ __forceinline__ void sharers(const Params &p, long long t, int &first, int &last) {
-    const long long t0 = t * p.chunks, t1 = t0 + p.chunks;
-    int c = blockIdx.x;
-    while (c > 0 && range_start(p, c) > t0) --c;
-    first = c;
-    c = blockIdx.x;
-    while (c + 1 < static_cast<int>(gridDim.x) && range_start(p, c + 1) < t1) ++c;
-    last = c;
+    auto owner = [&](long long u) { return static_cast<int>(((u + 1) * p.ranges + p.units - 1) / p.units - 1); };
+    first = owner(t * p.chunks);
+    last = owner((t + 1) * p.chunks - 1);
 }
 
-// Arrive on a shared tile's counter, the one of its first CTA (a CTA is the
-// first of one shared tile at most); true for the last arrival, which also
-// sets it back to zero.
+// Arrive on a shared tile's counter (each CTA of a pair has its own); true for
+// the last arrival, which also sets it back to zero.
+template <int CG>
 __device__ __forceinline__ bool arrive(const Params &p, int first, int last) {
-    uint32_t want = 0;
-    for (int c = first; c <= last; ++c) want += range_start(p, c) < range_start(p, c + 1) ? 1u : 0u;
-    if (atomicAdd(p.cnt + first, 1u) + 1 != want) return false;
-    atomicExch(p.cnt + first, 0u);
+    uint32_t *cnt = p.cnt + first * CG + blockIdx.x % CG;
+    if (atomicAdd(cnt, 1u) != static_cast<uint32_t>(last - first)) return false;
+    atomicExch(cnt, 0u);
     return true;
+}
+
+// Worker c's part of tile t (this CTA's rows): slot 1 for the tile that it
+// holds the first stage of, slot 0 for the one that its range starts inside.
+template <int CG>
+__device__ __forceinline__ int32_t *part_of(const Params &p, int c, long long t) {
+    const int slot = range_start(p, c) > t * p.chunks ? 0 : 1;
+    return p.part + ((static_cast<size_t>(c) * CG + blockIdx.x % CG) * 2 + slot) * p.tokens * kRows;
 }
 
 // A wait gave up: the caller's word says so, and the CTA unwinds.
@@ -173,16 +270,8 @@ __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ void put_y(const Params &p, long long m, long long n, float v) {
-    const size_t o = static_cast<size_t>(m) * static_cast<size_t>(p.N) + static_cast<size_t>(n);
-    if (p.y_f32)
-        static_cast<float *>(p.y)[o] = v;
-    else
-        static_cast<uint16_t *>(p.y)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
 // 32 TMEM lanes x 16 consecutive columns into 16 registers per thread.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, int32_t (&v)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15}, [%16];"
@@ -192,68 +281,124 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
         : "memory");
 }
 
-// The accumulators at `tmem` (this CTA's part [k0, k1) of tile w.tile): y, or
-// a part and, for the tile's last arrival, y from all parts.  Lane i of TMEM
-// is row i of the tile, a warp reads the 32 lanes of its quadrant.
+// Sixteen sums of one output channel, tokens m .. m + 15 of which the first
+// `here` exist: scaled and stored.  sx: the lane's token scale (lane i holds
+// that of token m + i).  `live`: the channel exists.
+__device__ __forceinline__ void put16(const Params &p, const int32_t (&v)[16], long long m, int here, long long n,
+                                      bool live, float sx, float sw) {
+    const size_t o = static_cast<size_t>(m) * static_cast<size_t>(p.N) + static_cast<size_t>(n);
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        f[i] = static_cast<float>(v[i]) * __shfl_sync(0xFFFFFFFFu, sx, i) * sw;
+    if (!live) return;
+    if (p.y_f32) {
+        float *y = static_cast<float *>(p.y) + o;
+#pragma unroll
+        for (int i = 0; i < 16; ++i, y += p.N)
+            if (i < here) *y = f[i];
+    } else {
+        uint16_t *y = static_cast<uint16_t *>(p.y) + o;
+#pragma unroll
+        for (int i = 0; i < 16; ++i, y += p.N)
+            if (i < here) *y = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+    }
+}
+
+// Add the other workers' parts of tile w.tile to sums v of tokens c .. c + 15
+// (the first `here` of them exist), PB parts in flight at a time.
+template <int CG, int PB, int NV>
+__device__ __forceinline__ void add_parts(const Params &p, int32_t (&v)[16], const Work &w, int first, int last,
+                                          int at, int here) {
+    for (int o = first; o <= last; o += PB) {
+        int32_t t[PB][NV];
+#pragma unroll
+        for (int b = 0; b < PB; ++b) {
+            const bool other = o + b <= last && o + b != static_cast<int>(blockIdx.x / CG);
+            const int32_t *src = part_of<CG>(p, other ? o + b : first, w.tile) + at;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) t[b][i] = other && i < here ? __ldcg(src + i * kRows) : 0;
+        }
+#pragma unroll
+        for (int b = 0; b < PB; ++b)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[i] += t[b][i];
+    }
+}
+
+// The accumulators at `tmem`, of this worker's stages of tile w.tile: y, or a
+// part and, for the tile's last arrival, y from all parts.  Lane i of TMEM is
+// this CTA's row i of the tile, a warp reads the 32 lanes of its quadrant.
+template <int CG>
 __device__ __forceinline__ void epilogue(const Params &p, const Layout &L, const Work &w, uint32_t tmem, int quad,
                                          int lane, uint32_t bar_empty) {
     const int row = quad * 32 + lane;
-    const long long n = w.tile / p.tiles_m * kRows + row, m0 = w.tile % p.tiles_m * p.tokens;
-    const bool whole = w.k0 == 0 && w.k1 == p.chunks;
-    const bool first_thread = quad == 0 && lane == 0;
-    const float sw = n < p.N ? __ldg(p.w_scale + n) : 0.f;
+    const long long n = (w.tile / p.tiles_m * CG + blockIdx.x % CG) * kRows + row, m0 = w.tile % p.tiles_m * p.tokens;
+    const int m_here = static_cast<int>(min(static_cast<long long>(p.tokens), p.M - m0));
+    const bool live = n < p.N;
+    const float sw = live ? __ldg(p.w_scale + n) : 0.f;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    // the CTA's range starts in this tile (slot 0) or reaches into it (1)
-    int32_t *mine = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (w.k0 > 0 ? 0 : 1)) * p.tokens * kRows;
-    for (int c = 0; c < p.tokens; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(taddr + static_cast<uint32_t>(c), v);
-        tmem_wait_ld();
+    int first = 0, last = 0;
+    bool store = true;
+    if (!w.whole(p)) {
+        sharers(p, w.tile, first, last);
+        int32_t *mine = part_of<CG>(p, blockIdx.x / CG, w.tile) + row;
+        for (int c = 0; c < m_here; c += 16) {
+            int32_t v[16];
+            tmem_ld16(taddr + static_cast<uint32_t>(c), v);
+            tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const long long m = m0 + c + i;
-            if (!whole)
-                __stcg(mine + static_cast<size_t>(c + i) * kRows + row, static_cast<int32_t>(v[i]));
-            else if (m < p.M && n < p.N)
-                put_y(p, m, n, static_cast<float>(static_cast<int32_t>(v[i])) * __ldg(p.x_scale + m) * sw);
+            for (int i = 0; i < 16; ++i)
+                if (c + i < m_here) __stcg(mine + (c + i) * kRows, v[i]);
+        }
+        __threadfence();
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+        if (quad == 0 && lane == 0) {
+            sts32(L.last, arrive<CG>(p, first, last) ? 1u : 0u);
+            sts32(L.shared_done, lds32(L.shared_done) + 1);
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+        store = lds32(L.last) != 0;
+        if (store) __threadfence();
+    }
+    if (store) {
+        auto token_scale = [&](int c) {
+            return c + (lane & 15) < m_here ? __ldg(p.x_scale + m0 + c + (lane & 15)) : 0.f;
+        };
+        float sx = token_scale(0);
+        for (int c = 0; c < m_here; c += 16) {
+            int32_t v[16];
+            tmem_ld16(taddr + static_cast<uint32_t>(c), v);
+            const float sx1 = token_scale(c + 16);
+            tmem_wait_ld();
+            if (first != last) {
+                if (m_here <= 4)
+                    add_parts<CG, 8, 4>(p, v, w, first, last, c * kRows + row, m_here);
+                else
+                    add_parts<CG, 4, 16>(p, v, w, first, last, c * kRows + row, m_here - c);
+            }
+            put16(p, v, m0 + c, m_here - c, n, live, sx, sw);
+            sx = sx1;
         }
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) bar_arrive(bar_empty);
-    if (whole) return;
-    __threadfence();
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
-    int first, last;
-    sharers(p, w.tile - p.tile0, first, last);
-    if (first_thread) {
-        sts32(L.last, arrive(p, first, last) ? 1u : 0u);
-        sts32(L.shared_done, lds32(L.shared_done) + 1);
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
-    if (!lds32(L.last)) return;
-    __threadfence();
-    const long long t0 = (w.tile - p.tile0) * p.chunks;
-    for (int c = 0; c < p.tokens; ++c) {
-        const long long m = m0 + c;
-        if (m >= p.M) break;
-        int32_t s = 0;
-        for (int v = first; v <= last; ++v) {
-            const long long vs = range_start(p, v);
-            if (vs < range_start(p, v + 1))
-                s += __ldcg(p.part + (static_cast<size_t>(v) * 2 + (vs > t0 ? 0 : 1)) * p.tokens * kRows +
-                            static_cast<size_t>(c) * kRows + row);
-        }
-        if (n < p.N) put_y(p, m, n, static_cast<float>(s) * __ldg(p.x_scale + m) * sw);
+    if (lane == 0) {
+        if (CG == 1)
+            bar_arrive(bar_empty);
+        else
+            arrive_at_leader(bar_empty);
     }
 }
 
+template <int CG>
 __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const Layout L = layout(sb);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.stages;
+    const uint32_t rank = CG == 1 ? 0u : cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             bar_init(L.full + 8 * s, 1);
@@ -261,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
         }
         for (int a = 0; a < 2; ++a) {
             bar_init(L.acc_full + 8 * a, 1);
-            bar_init(L.acc_empty + 8 * a, kEpiWarps);
+            bar_init(L.acc_empty + 8 * a, kEpiWarps * CG);
         }
         bar_init(L.done, 1);
         sts32(L.abort, 0u);
@@ -269,11 +414,19 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(L.tmem_slot, p.tmem_cols);
-        tmem_relinquish();
+        if (CG == 1) {
+            tmem_alloc(L.tmem_slot, p.tmem_cols);
+            tmem_relinquish();
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(L.tmem_slot),
+                         "r"(p.tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();  // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = lds32(L.tmem_slot);
     grid_launch_dependents();
@@ -285,20 +438,26 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
             uint32_t round = 0;
             long long issued = 0;
             bool ok = true;
-            Walk walk(p);
+            Walk<CG> walk(p);
+            const int x_rows = p.tokens / CG;
             for (Work w; ok && walk.next(p, w);) {
-                const int n0 = static_cast<int>(w.tile / p.tiles_m) * kRows;
-                const int m0 = static_cast<int>(w.tile % p.tiles_m) * p.tokens;
+                const int n0 = (static_cast<int>(w.tile / p.tiles_m) * CG + static_cast<int>(rank)) * kRows;
+                const int m0 = static_cast<int>(w.tile % p.tiles_m) * p.tokens + static_cast<int>(rank) * x_rows;
                 for (int k = w.k0; k < w.k1; ++k) {
                     if (!bar_wait(L.empty + 8 * s, (round & 1u) ^ 1u)) {
                         give_up(p, L.abort);
                         ok = false;
                         break;
                     }
-                    const uint32_t st = L.stages + static_cast<uint32_t>(s) * p.stage_bytes;
-                    bar_expect_tx(L.full + 8 * s, p.stage_bytes);
-                    tma2d(st, &p.tm_w, k * kChunk, n0, L.full + 8 * s, pol);
-                    tma2d(st + kWBytes, &p.tm_x, k * kChunk, m0, L.full + 8 * s, pol);
+                    const uint32_t st = L.stages + static_cast<uint32_t>(s) * p.stage_bytes, bar = L.full + 8 * s;
+                    if (rank == 0) bar_expect_tx(bar, CG * p.stage_bytes);
+                    if (CG == 1) {
+                        tma2d(st, &p.tm_w, k * kChunk, n0, bar, pol);
+                        tma2d(st + kWBytes, &p.tm_x, k * kChunk, m0, bar, pol);
+                    } else {
+                        tma2d_pair(st, &p.tm_w, k * kChunk, n0, leader_addr(bar), pol);
+                        tma2d_pair(st + kWBytes, &p.tm_x, k * kChunk, m0, leader_addr(bar), pol);
+                    }
                     ++issued;
                     if (++s == S) {
                         s = 0;
@@ -306,45 +465,49 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
                     }
                 }
             }
-            // every copy lands before the CTA leaves
-            for (long long i = issued > S ? issued - S : 0; i < issued; ++i)
-                bar_wait(L.full + 8 * static_cast<uint32_t>(i % S), static_cast<uint32_t>((i / S) & 1));
+            // every copy lands before the CTA leaves (the leader's barriers
+            // stand for both CTAs' copies)
+            if (rank == 0)
+                for (long long i = issued > S ? issued - S : 0; i < issued; ++i)
+                    bar_wait(L.full + 8 * static_cast<uint32_t>(i % S), static_cast<uint32_t>((i / S) & 1));
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = instr_desc(p.tokens);
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = instr_desc<CG>(p.tokens);
             int s = 0;
             uint32_t round = 0, tile = 0;
             bool ok = true;
-            Walk walk(p);
+            Walk<CG> walk(p);
             for (Work w; ok && walk.next(p, w); ++tile) {
                 const uint32_t a = tile & 1u;
-                ok = bar_wait(L.acc_empty + 8 * a, ((tile >> 1) & 1u) ^ 1u);
+                const uint32_t free_bar = L.acc_empty + 8 * a, free_par = ((tile >> 1) & 1u) ^ 1u;
+                ok = CG == 1 ? bar_wait(free_bar, free_par) : pair_wait(free_bar, free_par);
                 for (int k = w.k0; ok && k < w.k1; ++k) {
-                    if (!(ok = bar_wait(L.full + 8 * s, round & 1u))) break;
+                    ok = CG == 1 ? bar_wait(L.full + 8 * s, round & 1u) : pair_wait(L.full + 8 * s, round & 1u);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = L.stages + static_cast<uint32_t>(s) * p.stage_bytes;
 #pragma unroll
                     for (int kk = 0; kk < kChunk / 32; ++kk)
-                        umma_i8(tmem + a * p.acc_cols, smem_desc_sw128(st + 32u * kk),
-                                smem_desc_sw128(st + kWBytes + 32u * kk), idesc, k > w.k0 || kk > 0);
-                    umma_commit(L.empty + 8 * s);
+                        umma_i8<CG>(tmem + a * p.acc_cols, smem_desc_sw128(st + 32u * kk),
+                                    smem_desc_sw128(st + kWBytes + 32u * kk), idesc, k > w.k0 || kk > 0);
+                    commit<CG>(L.empty + 8 * s);
                     if (++s == S) {
                         s = 0;
                         ++round;
                     }
                 }
-                if (ok) umma_commit(L.acc_full + 8 * a);
+                if (ok) commit<CG>(L.acc_full + 8 * a);
             }
             if (!ok) give_up(p, L.abort);
             // every product issued has completed before TMEM is freed
-            umma_commit(L.done);
-            bar_wait(L.done, 0);
+            commit<CG>(L.done);
         }
+        if (lane == 0) bar_wait(L.done, 0);
     } else {
         const int quad = warp & 3;  // the TMEM lanes that this warp may read
         uint32_t tile = 0;
-        Walk walk(p);
+        Walk<CG> walk(p);
         for (Work w; walk.next(p, w); ++tile) {
             const uint32_t a = tile & 1u;
             const bool ok = bar_wait(L.acc_full + 8 * a, (tile >> 1) & 1u);
@@ -363,27 +526,34 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
                 break;
             }
             tc_fence_after();
-            epilogue(p, L, w, tmem + a * p.acc_cols, quad, lane, L.acc_empty + 8 * a);
+            epilogue<CG>(p, L, w, tmem + a * p.acc_cols, quad, lane, L.acc_empty + 8 * a);
         }
     }
     __syncthreads();
+    // (the other CTA's products read this one's shared memory, its arrivals
+    // go to this one's barriers)
+    if (CG == 2) cluster_sync();
     if (warp == 1) {
+        __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, p.tmem_cols);
+        if (CG == 1)
+            tmem_dealloc(tmem, p.tmem_cols);
+        else
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols)
+                         : "memory");
     }
     if (threadIdx.x == 0 && lds32(L.abort)) {
         // the shared tiles that this CTA did not get to still see its
         // arrival, so that their counters return to zero
         const uint32_t done = lds32(L.shared_done);
         uint32_t k = 0;
-        Walk walk(p);
+        Walk<CG> walk(p);
         walk.wave = p.waves;
         for (Work w; walk.next(p, w);) {
-            if (w.k0 == 0 && w.k1 == p.chunks) continue;
-            if (k++ < done) continue;
+            if (w.whole(p) || k++ < done) continue;
             int first, last;
-            sharers(p, w.tile - p.tile0, first, last);
-            arrive(p, first, last);
+            sharers(p, w.tile, first, last);
+            arrive<CG>(p, first, last);
         }
     }
 }
@@ -396,23 +566,58 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
 namespace {
 
 constexpr uint32_t kSmemLimit = 227 * 1024;
+constexpr int kPairTokens = 128;  // more tokens than this: two CTAs a product
 
 struct Plan8 {
-    int tokens, tiles_m;
+    int cg, tokens, tiles_m;
     size_t cnt_bytes, part_bytes;
 };
 
 Plan8 plan8(int64_t M, int sms) {
     Plan8 pl;
-    // token tiles of equal size, as few as 256 rows allow
-    const int64_t tiles = (M + gemm8::kMaxTokens - 1) / gemm8::kMaxTokens;
+    pl.cg = M > kPairTokens ? 2 : 1;
+    // token tiles of equal size, as few as 256 tokens each allow
+    const int64_t tiles = (M + gemm8::kMaxTokens - 1) / gemm8::kMaxTokens, step = 16 * pl.cg;
     pl.tiles_m = static_cast<int>(tiles);
-    pl.tokens = static_cast<int>(((M + tiles - 1) / tiles + 15) / 16 * 16);
+    pl.tokens = static_cast<int>(((M + tiles - 1) / tiles + step - 1) / step * step);
     // the counters first and their size by the device alone: calls of other
     // shapes may use the workspace in turn
     pl.cnt_bytes = align_up(static_cast<uint64_t>(sms) * 4, kAlign);
     pl.part_bytes = static_cast<size_t>(sms) * 2 * pl.tokens * gemm8::kRows * 4;
     return pl;
+}
+
+// How many workers the `rest` tiles before the whole waves are dealt to, of
+// `workers` in all.  Dealing evens the load out: it saves about chunks * (1 -
+// rest / workers) stages, each of which takes its bytes at some 53 a cycle.
+// Joining the parts costs some 3000 cycles and 20 a token.  Where that is
+// more, a tile stays whole.
+int ranges_of(int rest, int workers, int chunks, uint32_t stage_bytes, int tokens) {
+    if (rest == 0) return 0;
+    const int ranges = static_cast<int>(
+        std::min<long long>({workers, static_cast<long long>(rest) * gemm8::kShare, static_cast<long long>(rest) * chunks}));
+    const double saved = chunks * (1.0 - static_cast<double>(rest) / ranges) * stage_bytes / 53.0;
+    return saved > 3000.0 + 20.0 * tokens ? ranges : rest;
+}
+
+template <int CG>
+int run8(const gemm8::Params &p, int workers, uint32_t smem, cudaStream_t stream) {
+    auto kern = gemm8::gemm_i8_kernel<CG>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return S12_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(workers * CG);
+    cfg.blockDim = dim3(gemm8::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {CG, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = CG;  // (a cluster only for pairs)
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? S12_OK : S12_ERR_CUDA;
 }
 
 }  // namespace
@@ -431,7 +636,7 @@ int launch_gemm_i8(const Gemm8Call &c, void *ws, size_t ws_bytes, cudaStream_t s
     if (ws_bytes < pl.cnt_bytes + pl.part_bytes) return S12_ERR_CAPACITY;
     gemm8::Params p = {};
     if (make_tmap_u8_2d(&p.tm_w, c.w, c.K, c.N, c.K, gemm8::kChunk, gemm8::kRows, 128) != S12_OK ||
-        make_tmap_u8_2d(&p.tm_x, c.x, c.K, c.M, c.K, gemm8::kChunk, pl.tokens, 128) != S12_OK)
+        make_tmap_u8_2d(&p.tm_x, c.x, c.K, c.M, c.K, gemm8::kChunk, pl.tokens / pl.cg, 128) != S12_OK)
         return S12_ERR_CUDA;
     p.x_scale = c.x_scale;
     p.w_scale = c.w_scale;
@@ -443,32 +648,22 @@ int launch_gemm_i8(const Gemm8Call &c, void *ws, size_t ws_bytes, cudaStream_t s
     p.tokens = pl.tokens;
     p.chunks = static_cast<int>((c.K + gemm8::kChunk - 1) / gemm8::kChunk);
     p.tiles_m = pl.tiles_m;
-    const long long tiles = (c.N + gemm8::kRows - 1) / gemm8::kRows * pl.tiles_m;
-    const int grid = static_cast<int>(std::min<long long>(sms, tiles * p.chunks));
-    p.waves = static_cast<int>(tiles / grid);
-    p.tile0 = static_cast<long long>(p.waves) * grid;
-    p.units = (tiles - p.tile0) * p.chunks;
+    const int rows = gemm8::kRows * pl.cg, all = sms / pl.cg;
+    const long long tiles = (c.N + rows - 1) / rows * pl.tiles_m;
+    p.stage_bytes = gemm8::kWBytes + static_cast<uint32_t>(pl.tokens / pl.cg) * gemm8::kChunk;
+    p.waves = static_cast<int>(tiles / all);
+    p.rest = static_cast<int>(tiles % all);
+    p.units = static_cast<long long>(p.rest) * p.chunks;
+    p.ranges = ranges_of(p.rest, all, p.chunks, p.stage_bytes, pl.tokens);
+    const int workers = p.waves ? all : p.ranges;
     p.cnt = static_cast<uint32_t *>(ws);
     p.part = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + pl.cnt_bytes);
-    p.stage_bytes = gemm8::kWBytes + static_cast<uint32_t>(pl.tokens) * gemm8::kChunk;
     p.stages = static_cast<int>(std::min<uint32_t>(gemm8::kMaxStages, (kSmemLimit - 2048) / p.stage_bytes));
     p.acc_cols = 32;
     while (p.acc_cols < static_cast<uint32_t>(pl.tokens)) p.acc_cols <<= 1;
     p.tmem_cols = 2 * p.acc_cols;
     const uint32_t smem = 2048 + static_cast<uint32_t>(p.stages) * p.stage_bytes;
-    if (cudaFuncSetAttribute(gemm8::gemm_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return S12_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(gemm8::kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm8::gemm_i8_kernel, p) == cudaSuccess ? S12_OK : S12_ERR_CUDA;
+    return pl.cg == 1 ? run8<1>(p, workers, smem, stream) : run8<2>(p, workers, smem, stream);
 }
 
 }  // namespace s12
