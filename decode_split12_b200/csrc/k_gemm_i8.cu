@@ -9,10 +9,11 @@
 // single token (N = 16: bound by reading W) and prompts (bound by the tensor
 // cores).
 //
-// One CTA per SM, six warps with fixed roles: a TMA producer (128 columns of W
+// One CTA per SM, ten warps with fixed roles: a TMA producer (128 columns of W
 // and X a stage, 128-byte swizzle), the MMA issuer (four tcgen05.mma.kind::i8
-// of K = 32 a stage), and four epilogue warps that read the accumulators from
-// TMEM, scale and store them.  There are two accumulators, so that the next
+// of K = 32 a stage), and eight epilogue warps that read the accumulators from
+// TMEM, scale and store them (two to a scheduler: one alone waits for its own
+// results most of the time).  There are two accumulators, so that the next
 // tile is multiplied while one is stored.
 //
 // CG = 1: a CTA multiplies 128 rows of W.  CG = 2 (more than 128 tokens): two
@@ -21,7 +22,7 @@
 // at 128 x 256 x 128 the tensor cores take a stage faster than L2 delivers 48.
 //
 // Work split.  The tiles that fill no whole wave of the grid come first: their
-// stages are dealt to the CTAs in equal ranges, at most kShare ranges a tile.
+// stages are dealt to the CTAs in equal ranges, a few of them a tile.
 // The whole waves follow, one tile to a CTA, neighbours at the same time (they
 // share rows of W or X in L2), and hide the joining of the shared tiles.  A
 // CTA that holds a part of a tile writes its sums to the workspace; the last
@@ -44,8 +45,7 @@ constexpr int kRows = 128;    // rows of W per tile (UMMA M)
 constexpr int kChunk = 128;   // columns per stage: one swizzle atom
 constexpr int kMaxTokens = 256;
 constexpr int kMaxStages = 12;
-constexpr int kEpiWarps = 4;
-constexpr int kShare = 8;     // ranges that a shared tile is cut into at most
+constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr uint32_t kWBytes = kRows * kChunk;
 
@@ -225,12 +225,11 @@ __device__ __forceinline__ bool arrive(const Params &p, int first, int last) {
     return true;
 }
 
-// Worker c's part of tile t (this CTA's rows): slot 1 for the tile that it
-// holds the first stage of, slot 0 for the one that its range starts inside.
+// Worker c's part of a shared tile (this CTA's rows): slot 1 for the tile that
+// it is the first of, slot 0 for the one that its range starts inside.
 template <int CG>
-__device__ __forceinline__ int32_t *part_of(const Params &p, int c, long long t) {
-    const int slot = range_start(p, c) > t * p.chunks ? 0 : 1;
-    return p.part + ((static_cast<size_t>(c) * CG + blockIdx.x % CG) * 2 + slot) * p.tokens * kRows;
+__device__ __forceinline__ int32_t *part_of(const Params &p, int c, bool is_first) {
+    return p.part + ((static_cast<size_t>(c) * CG + blockIdx.x % CG) * 2 + (is_first ? 1 : 0)) * p.tokens * kRows;
 }
 
 // A wait gave up: the caller's word says so, and the CTA unwinds.
@@ -305,17 +304,16 @@ __device__ __forceinline__ void put16(const Params &p, const int32_t (&v)[16], l
     }
 }
 
-// Add the other workers' parts of tile w.tile to sums v of tokens c .. c + 15
-// (the first `here` of them exist), PB parts in flight at a time.
+// Add the other workers' parts of a tile, from place `at` on, to sums v of 16
+// tokens of which the first `here` exist; PB parts of NV tokens in flight.
 template <int CG, int PB, int NV>
-__device__ __forceinline__ void add_parts(const Params &p, int32_t (&v)[16], const Work &w, int first, int last,
-                                          int at, int here) {
+__device__ __forceinline__ void add_parts(const Params &p, int32_t (&v)[16], int first, int last, int at, int here) {
     for (int o = first; o <= last; o += PB) {
         int32_t t[PB][NV];
 #pragma unroll
         for (int b = 0; b < PB; ++b) {
             const bool other = o + b <= last && o + b != static_cast<int>(blockIdx.x / CG);
-            const int32_t *src = part_of<CG>(p, other ? o + b : first, w.tile) + at;
+            const int32_t *src = part_of<CG>(p, other ? o + b : first, o + b == first) + at;
 #pragma unroll
             for (int i = 0; i < NV; ++i) t[b][i] = other && i < here ? __ldcg(src + i * kRows) : 0;
         }
@@ -328,10 +326,11 @@ __device__ __forceinline__ void add_parts(const Params &p, int32_t (&v)[16], con
 
 // The accumulators at `tmem`, of this worker's stages of tile w.tile: y, or a
 // part and, for the tile's last arrival, y from all parts.  Lane i of TMEM is
-// this CTA's row i of the tile, a warp reads the 32 lanes of its quadrant.
+// this CTA's row i of the tile; a warp reads the 32 lanes of its quadrant, and
+// every second sixteen tokens (`odd`: the second ones).
 template <int CG>
 __device__ __forceinline__ void epilogue(const Params &p, const Layout &L, const Work &w, uint32_t tmem, int quad,
-                                         int lane, uint32_t bar_empty) {
+                                         int odd, int lane, uint32_t bar_empty) {
     const int row = quad * 32 + lane;
     const long long n = (w.tile / p.tiles_m * CG + blockIdx.x % CG) * kRows + row, m0 = w.tile % p.tiles_m * p.tokens;
     const int m_here = static_cast<int>(min(static_cast<long long>(p.tokens), p.M - m0));
@@ -342,8 +341,8 @@ __device__ __forceinline__ void epilogue(const Params &p, const Layout &L, const
     bool store = true;
     if (!w.whole(p)) {
         sharers(p, w.tile, first, last);
-        int32_t *mine = part_of<CG>(p, blockIdx.x / CG, w.tile) + row;
-        for (int c = 0; c < m_here; c += 16) {
+        int32_t *mine = part_of<CG>(p, blockIdx.x / CG, w.k0 == 0) + row;
+        for (int c = 16 * odd; c < m_here; c += 32) {
             int32_t v[16];
             tmem_ld16(taddr + static_cast<uint32_t>(c), v);
             tmem_wait_ld();
@@ -353,7 +352,7 @@ __device__ __forceinline__ void epilogue(const Params &p, const Layout &L, const
         }
         __threadfence();
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
-        if (quad == 0 && lane == 0) {
+        if (quad == 0 && odd == 0 && lane == 0) {
             sts32(L.last, arrive<CG>(p, first, last) ? 1u : 0u);
             sts32(L.shared_done, lds32(L.shared_done) + 1);
         }
@@ -365,17 +364,17 @@ __device__ __forceinline__ void epilogue(const Params &p, const Layout &L, const
         auto token_scale = [&](int c) {
             return c + (lane & 15) < m_here ? __ldg(p.x_scale + m0 + c + (lane & 15)) : 0.f;
         };
-        float sx = token_scale(0);
-        for (int c = 0; c < m_here; c += 16) {
+        float sx = token_scale(16 * odd);
+        for (int c = 16 * odd; c < m_here; c += 32) {
             int32_t v[16];
             tmem_ld16(taddr + static_cast<uint32_t>(c), v);
-            const float sx1 = token_scale(c + 16);
+            const float sx1 = token_scale(c + 32);
             tmem_wait_ld();
             if (first != last) {
                 if (m_here <= 4)
-                    add_parts<CG, 8, 4>(p, v, w, first, last, c * kRows + row, m_here);
+                    add_parts<CG, 8, 4>(p, v, first, last, c * kRows + row, m_here);
                 else
-                    add_parts<CG, 4, 16>(p, v, w, first, last, c * kRows + row, m_here - c);
+                    add_parts<CG, 4, 16>(p, v, first, last, c * kRows + row, m_here - c);
             }
             put16(p, v, m0 + c, m_here - c, n, live, sx, sw);
             sx = sx1;
@@ -505,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
         }
         if (lane == 0) bar_wait(L.done, 0);
     } else {
-        const int quad = warp & 3;  // the TMEM lanes that this warp may read
+        const int quad = warp & 3, odd = (warp - 2) >> 2;  // the TMEM lanes that this warp may read, its tokens
         uint32_t tile = 0;
         Walk<CG> walk(p);
         for (Work w; walk.next(p, w); ++tile) {
@@ -526,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
                 break;
             }
             tc_fence_after();
-            epilogue<CG>(p, L, w, tmem + a * p.acc_cols, quad, lane, L.acc_empty + 8 * a);
+            epilogue<CG>(p, L, w, tmem + a * p.acc_cols, quad, odd, lane, L.acc_empty + 8 * a);
         }
     }
     __syncthreads();
@@ -590,14 +589,16 @@ Plan8 plan8(int64_t M, int sms) {
 // How many workers the `rest` tiles before the whole waves are dealt to, of
 // `workers` in all.  Dealing evens the load out: it saves about chunks * (1 -
 // rest / workers) stages, each of which takes its bytes at some 53 a cycle.
-// Joining the parts costs some 3000 cycles and 20 a token.  Where that is
-// more, a tile stays whole.
+// Joining costs some 3000 cycles, and 20 a token for each part; where that is
+// more, a tile stays whole, and the parts of large tiles are few.
 int ranges_of(int rest, int workers, int chunks, uint32_t stage_bytes, int tokens) {
     if (rest == 0) return 0;
+    const int share = tokens <= 64 ? 8 : 4;
     const int ranges = static_cast<int>(
-        std::min<long long>({workers, static_cast<long long>(rest) * gemm8::kShare, static_cast<long long>(rest) * chunks}));
+        std::min<long long>({workers, static_cast<long long>(rest) * share, static_cast<long long>(rest) * chunks}));
     const double saved = chunks * (1.0 - static_cast<double>(rest) / ranges) * stage_bytes / 53.0;
-    return saved > 3000.0 + 20.0 * tokens ? ranges : rest;
+    const double parts = static_cast<double>(ranges) / rest;
+    return saved > 3000.0 + 20.0 * tokens * parts ? ranges : rest;
 }
 
 template <int CG>
