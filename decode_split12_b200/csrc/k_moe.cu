@@ -58,9 +58,9 @@ using namespace stage;
 constexpr int kWarps = 16;   // warps per CTA, one CTA per SM
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 2;   // stages per warp ring
-constexpr int kSeg = 64;     // (token, slot) pairs that share one read of an expert's weights
+constexpr int kSegSmall = 8, kSegLarge = 64;  // (token, slot) pairs that share one read of an expert's weights
 constexpr int kMaxSlots = S12_MOE_MAX_TOKENS * S12_MOE_MAX_TOP_K;
-constexpr int kMaxSegs = S12_MOE_MAX_EXPERTS + kMaxSlots / kSeg;
+constexpr int kMaxSegs = S12_MOE_MAX_EXPERTS + kMaxSlots / kSegSmall;
 constexpr uint32_t kPartBytes = 512;  // one warp's sums of 16 rows x 8 tokens
 constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
 
@@ -78,7 +78,7 @@ struct __align__(64) Mat {
 };
 
 // Words that the grid meets at.
-enum { kBarRoute = 0, kBarHidden = 1, kExits = 2, kAbort = 3, kSyncWords = 4 };
+enum { kBarRoute, kBarSums, kBarHidden, kBarDown, kNext1, kNext2, kExits, kAbort, kSyncWords };
 
 struct __align__(64) Params {
     Mat up, down;
@@ -91,13 +91,18 @@ struct __align__(64) Params {
     uint32_t *err;
     int tokens, experts, top_k, H, F;
     int renorm, y_f32;
+    int seg;         // pairs of a segment at most
+    // the kernel for few tokens:
+    int local;       // every CTA routes for itself, with x in shared memory
+    uint32_t range_up, range_down;  // stages of an item
     // workspace
     uint32_t *sync;         // kSyncWords
     uint32_t *cnt;          // arrivals: [segs][G up], [segs][G down], [G down]
     uint32_t n_cnt, cnt_down, cnt_y;
     double *scores;         // [tokens][experts]
     uint8_t *xp, *hi, *lo;  // x, and h as two BF16 values, in the products' order
-    float *d;               // [slots][H]
+    float *gu;              // few tokens: [ranges][slots][2F]
+    float *d;               // [slots][H], few tokens: [ranges][slots][H]
     float *warp_part;       // [CTAs * kWarps][2][NT][128] for more than 8 tokens an expert
     float *cta_part;        // [CTAs][2][NT][128]
 };
@@ -107,6 +112,8 @@ struct Shared {
     float weight[kMaxSlots];
     int16_t expert[kMaxSlots];  // of each (token, slot), -1 for none
     uint16_t list[kMaxSlots];   // (token, slot) pairs by expert
+    uint16_t token[kMaxSlots];  // of each of them
+    uint16_t place[kMaxSlots];  // of each (token, slot) in the list
     int count[S12_MOE_MAX_EXPERTS], first[S12_MOE_MAX_EXPERTS];
     uint16_t seg_expert[kMaxSegs], seg_first[kMaxSegs];
     uint8_t seg_n[kMaxSegs];
@@ -166,14 +173,14 @@ __device__ __forceinline__ bool grid_meet(const Params &p, Shared *sm, int word)
 // ---------------------------------------------------------------------------
 // Step 0: x in the products' order, scores, experts.
 
-__device__ __forceinline__ void pack_x(const Params &p) {
+__device__ __forceinline__ void pack_x(const Params &p, uint8_t *to, int i0, int step) {
     const int per_row = p.H / 8;
     const int n = p.tokens * per_row;
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) {
+    for (int i = i0; i < n; i += step) {
         const int t = i / per_row, c8 = i - t * per_row;  // piece c8 of token t
         const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.x) + i);
         const int in = c8 & 15;  // piece of the tile: 64 columns, chunk, half
-        uint4 *dst = reinterpret_cast<uint4 *>(p.xp + piece_at(c8 >> 4, (in >> 1) & 3, in & 1, p.tokens, t, in >> 3));
+        uint4 *dst = reinterpret_cast<uint4 *>(to + piece_at(c8 >> 4, (in >> 1) & 3, in & 1, p.tokens, t, in >> 3));
         *dst = make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u),
                           prmt(v.y, v.w, 0x7632u));
     }
@@ -192,17 +199,17 @@ __device__ __forceinline__ void unpack8(const uint4 &a, float (&v)[8]) {
 // are exact in FP32; eight of them are added in FP32, the rest in 64 bits,
 // because the choice of experts hangs on the order of the scores.
 template <int TT, int TE>
-__device__ __forceinline__ void score(const Params &p) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ void score(const Params &p, double *scores, int u0, int step) {
+    const int lane = threadIdx.x & 31;
     const int nt = (p.tokens + TT - 1) / TT, ne = (p.experts + TE - 1) / TE;
-    for (int u = warp * gridDim.x + blockIdx.x; u < nt * ne; u += gridDim.x * kWarps) {
+    for (int u = u0; u < nt * ne; u += step) {
         const int t0 = u / ne * TT, e0 = u % ne * TE;
         double acc[TT][TE];
 #pragma unroll
         for (int i = 0; i < TT; ++i)
 #pragma unroll
             for (int j = 0; j < TE; ++j) acc[i][j] = 0.0;
-#pragma unroll(TT == 1 ? 4 : 1)
+#pragma unroll(TT == 1 ? 8 : 1)
         for (int k = lane * 8; k < p.H; k += 256) {
             float xv[TT][8];
 #pragma unroll
@@ -232,7 +239,7 @@ __device__ __forceinline__ void score(const Params &p) {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
                 if (lane == 0 && t0 + i < p.tokens && e0 + j < p.experts)
-                    p.scores[static_cast<size_t>(t0 + i) * p.experts + e0 + j] = s;
+                    scores[static_cast<size_t>(t0 + i) * p.experts + e0 + j] = s;
             }
     }
 }
@@ -240,10 +247,10 @@ __device__ __forceinline__ void score(const Params &p) {
 // The experts and weights of token t, by one warp: the top_k largest scores,
 // the lower index first where two are equal (a NaN counts as -infinity, and
 // makes the token's weights NaN).
-__device__ __forceinline__ void select_experts(const Params &p, Shared *sm, int t) {
+__device__ __forceinline__ void select_experts(const Params &p, Shared *sm, const double *scores, int t) {
     constexpr int kPer = S12_MOE_MAX_EXPERTS / 32;
     const int lane = threadIdx.x & 31;
-    const double *row = p.scores + static_cast<size_t>(t) * p.experts;
+    const double *row = scores + static_cast<size_t>(t) * p.experts;
     const double low = -__longlong_as_double(0x7FF0000000000000ll);
     double v[kPer];
     uint32_t left = 0u;  // bit i: expert lane + 32 i is not chosen yet
@@ -252,7 +259,7 @@ __device__ __forceinline__ void select_experts(const Params &p, Shared *sm, int 
         const int e = lane + 32 * i;
         v[i] = low;
         if (e < p.experts) {
-            v[i] = __ldcg(row + e);
+            v[i] = row[e];
             if (v[i] != v[i]) v[i] = low;
             left |= 1u << i;
         }
@@ -307,8 +314,8 @@ __device__ __forceinline__ void select_experts(const Params &p, Shared *sm, int 
 }
 
 // Every CTA for itself: the (token, slot) pairs sorted by expert (by index
-// inside one), cut into segments of at most kSeg.
-__device__ __forceinline__ void route(const Params &p, Shared *sm) {
+// inside one), cut into segments of at most p.seg.
+__device__ __forceinline__ void route(const Params &p, Shared *sm, const double *scores) {
     const int slots = p.tokens * p.top_k, tid = threadIdx.x;
     if (p.ids_in) {
         if (tid < slots) {
@@ -317,7 +324,7 @@ __device__ __forceinline__ void route(const Params &p, Shared *sm) {
             sm->weight[tid] = __ldg(p.weights_in + tid);
         }
     } else {
-        for (int t = tid >> 5; t < p.tokens; t += kWarps) select_experts(p, sm, t);
+        for (int t = tid >> 5; t < p.tokens; t += kWarps) select_experts(p, sm, scores, t);
     }
     __syncthreads();
     if (tid < p.experts) {
@@ -333,8 +340,8 @@ __device__ __forceinline__ void route(const Params &p, Shared *sm) {
         for (int i = 0; i < kPer; ++i) {
             const int e = tid * kPer + i, n = e < p.experts ? sm->count[e] : 0;
             pairs += n;
-            segs += (n + kSeg - 1) / kSeg;
-            most = max(most, min(n, kSeg));
+            segs += (n + p.seg - 1) / p.seg;
+            most = max(most, min(n, p.seg));
         }
         int pairs_to = pairs, segs_to = segs;
 #pragma unroll
@@ -349,10 +356,10 @@ __device__ __forceinline__ void route(const Params &p, Shared *sm) {
         for (int i = 0; i < kPer; ++i) {
             const int e = tid * kPer + i, n = e < p.experts ? sm->count[e] : 0;
             if (e < p.experts) sm->first[e] = at;
-            for (int k = 0; k < n; k += kSeg, ++seg) {
+            for (int k = 0; k < n; k += p.seg, ++seg) {
                 sm->seg_expert[seg] = static_cast<uint16_t>(e);
                 sm->seg_first[seg] = static_cast<uint16_t>(at + k);
-                sm->seg_n[seg] = static_cast<uint8_t>(min(n - k, kSeg));
+                sm->seg_n[seg] = static_cast<uint8_t>(min(n - k, p.seg));
             }
             at += n;
         }
@@ -366,7 +373,11 @@ __device__ __forceinline__ void route(const Params &p, Shared *sm) {
     if (tid < p.experts && sm->count[tid]) {
         int at = sm->first[tid];
         for (int i = 0; i < slots; ++i)
-            if (sm->expert[i] == tid) sm->list[at++] = static_cast<uint16_t>(i);
+            if (sm->expert[i] == tid) {
+                sm->place[i] = static_cast<uint16_t>(at);
+                sm->token[at] = static_cast<uint16_t>(i / p.top_k);
+                sm->list[at++] = static_cast<uint16_t>(i);
+            }
     }
     __syncthreads();
 }
@@ -447,6 +458,27 @@ __device__ __forceinline__ void issue(const Params &p, const Shared *sm, Ring &r
     }
     ++r.issued;
     advance<PH>(p, sm, c);
+}
+
+// The end of a CTA: copies that a wait left in flight land, and the last CTA
+// leaves the workspace's words at zero.
+__device__ __forceinline__ void finish(const Params &p, Shared *sm, const Ring &rg) {
+    if ((threadIdx.x & 31) == 0)
+        for (int k = rg.consumed; k < rg.issued; ++k)
+            mbar_wait_s(rg.bars + 8u * (k & 1), static_cast<uint32_t>(k >> 1) & 1u);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        sm->last = atomicAdd(p.sync + kExits, 1u) + 1 == gridDim.x;
+    }
+    __syncthreads();
+    if (sm->last) {
+        __threadfence();
+        if (ld_acquire(p.sync + kAbort))
+            for (uint32_t i = threadIdx.x; i < p.n_cnt; i += kThreads) p.cnt[i] = 0u;
+        __syncthreads();
+        if (threadIdx.x < kSyncWords) p.sync[threadIdx.x] = 0u;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -939,16 +971,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         for (int s = 0; s < kStages; ++s) mbar_init_s(rg.bars + 8u * s, 1);
         fence_barrier_init();
     }
-    pack_x(p);
+    pack_x(p, p.xp, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
     if (!p.ids_in) {
         // many scores: 4 x 4 to a warp, so that x and the router are read a quarter as often
+        const int u0 = warp * gridDim.x + blockIdx.x, step = gridDim.x * kWarps;
         if (p.tokens >= 8 && p.tokens * p.experts >= 1024)
-            score<4, 4>(p);
+            score<4, 4>(p, p.scores, u0, step);
         else
-            score<1, 1>(p);
+            score<1, 1>(p, p.scores, u0, step);
     }
     if (grid_meet(p, sm, kBarRoute)) {
-        route(p, sm);
+        route(p, sm, p.scores);
         if (sm->n_segs == 0) {
             // no token goes anywhere
             const size_t n = static_cast<size_t>(p.tokens) * p.H;
@@ -963,23 +996,491 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             rg = layer<V, 8>(p, sm, parts, rg);
         }
     }
-    // copies that a wait left in flight land before the CTA leaves
-    if (lane == 0)
-        for (int k = rg.consumed; k < rg.issued; ++k)
-            mbar_wait_s(rg.bars + 8u * (k & 1), static_cast<uint32_t>(k >> 1) & 1u);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        sm->last = atomicAdd(p.sync + kExits, 1u) + 1 == gridDim.x;
+    finish(p, sm, rg);
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens an expert: at most eight pairs share a read of an expert's
+// weights.
+//
+// An item is a row group by a few stages of its columns.  Warps take items as
+// they come for them (two are known in advance, the rest come from a counter
+// of the grid), and write an item's sums to its place in the workspace, where
+// the next step adds up the ranges of a row group in their order.  So warps
+// never wait for one another inside a step, every SM works until the items are
+// gone (dealt in equal ranges, the slowest SM took a fifth longer than the
+// average), and which warp has which item does not change any sum.  The price
+// is 64 bytes written a pair for 6 KB of weights or more, and a meeting of the
+// grid before and after the sums of step 1; the first weights of step 2 are
+// copied meanwhile.
+
+struct Step {
+    uint32_t items;      // of the step: row groups by ranges
+    uint32_t stages;     // of a range (the last range of a row group may have fewer)
+    uint32_t ranges;     // of a row group
+    uint32_t m1, m2, d2;  // reciprocals of `ranges` and of d2, the row groups (step 1) or segments (step 2)
+};
+
+struct SmallShared {
+    Shared s;
+    Step step[2];
+};
+
+// n / d with m = ceil(2^32 / d): the product is at most one too large.
+__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t m, uint32_t d) {
+    const uint32_t q = d == 1 ? n : __umulhi(n, m);
+    return q * d > n ? q - 1 : q;
+}
+
+__device__ __forceinline__ uint32_t reciprocal(uint32_t d) {
+    return static_cast<uint32_t>(((1ull << 32) + d - 1) / d);
+}
+
+struct Item {
+    uint32_t seg, grp, range;
+};
+
+template <int PH>
+__device__ __forceinline__ Item item_at(const Step &st, uint32_t it) {
+    const uint32_t t = divide(it, st.m1, st.ranges), u = divide(t, st.m2, st.d2), v = t - u * st.d2;
+    Item o;
+    o.range = it - t * st.ranges;
+    o.seg = PH == 1 ? u : v;  // step 1 by segments, step 2 by row groups
+    o.grp = PH == 1 ? v : u;
+    return o;
+}
+
+template <int PH>
+__device__ __forceinline__ void plan_step(const Params &p, SmallShared *sm) {
+    const Mat &m = mat<PH>(p);
+    Step st;
+    const uint32_t groups = static_cast<uint32_t>(sm->s.n_segs) * m.G;
+    st.stages = min(PH == 1 ? p.range_up : p.range_down, m.S);
+    st.ranges = (m.S + st.stages - 1) / st.stages;
+    st.items = groups * st.ranges;
+    st.d2 = PH == 1 ? static_cast<uint32_t>(m.G) : static_cast<uint32_t>(sm->s.n_segs);
+    st.m1 = reciprocal(st.ranges);
+    st.m2 = reciprocal(st.d2);
+    sm->step[PH - 1] = st;
+}
+
+// One stage of a warp.
+struct Desc {
+    uint32_t row16;  // 16-row group of the matrix
+    int j;           // first tile
+    uint32_t it;     // item of the step
+    bool live, last;  // a stage at all; the item's last
+};
+
+// The warp's way through a step.
+template <int PH>
+struct Feed {
+    uint32_t it, ahead;  // the item at hand, and the one after it (lane 0 knows)
+    uint32_t s, n;       // its next stage, and its stages
+    uint32_t row16;
+    int j;               // first tile of the item
+
+    __device__ __forceinline__ void take(const Params &p, const SmallShared *sm, uint32_t item) {
+        const Step &st = sm->step[PH - 1];
+        const Mat &m = mat<PH>(p);
+        it = item;
+        s = n = 0;
+        if (it >= st.items) return;
+        const Item at = item_at<PH>(st, it);
+        n = min(st.stages, m.S - at.range * st.stages);
+        row16 = sm->s.seg_expert[at.seg] * static_cast<uint32_t>(m.G) + at.grp;
+        j = static_cast<int>(at.range * st.stages) * kNT;
     }
-    __syncthreads();
-    if (sm->last) {
-        __threadfence();
-        if (ld_acquire(p.sync + kAbort))
-            for (uint32_t i = threadIdx.x; i < p.n_cnt; i += kThreads) p.cnt[i] = 0u;
+
+    __device__ __forceinline__ void start(const Params &p, const SmallShared *sm) {
+        const uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);  // (neighbours share metadata)
+        take(p, sm, u);
+        ahead = u + gridDim.x * kWarps;
+    }
+
+    __device__ __forceinline__ Desc next(const Params &p, const SmallShared *sm) {
+        if (s == n && n != 0) {
+            take(p, sm, __shfl_sync(0xFFFFFFFFu, ahead, 0));
+            // (the answer is not needed before the next item)
+            if ((threadIdx.x & 31) == 0)
+                ahead = 2 * gridDim.x * kWarps + atomicAdd(p.sync + (PH == 1 ? kNext1 : kNext2), 1u);
+        }
+        Desc d;
+        d.live = s < n;
+        d.row16 = row16;
+        d.j = j + static_cast<int>(s) * kNT;
+        d.it = it;
+        d.last = s + 1 == n;
+        if (d.live) ++s;
+        return d;
+    }
+};
+
+template <int PH>
+__device__ __forceinline__ void issue_at(const Params &p, Ring &r, const Desc &d) {
+    if ((threadIdx.x & 31) == 0) {
+        const uint32_t s = static_cast<uint32_t>(r.issued & 1), st = r.base + s * kStageBytes, bar = r.bars + 8u * s;
+        const uint64_t pol = policy_evict_first();
+        const Mat &m = mat<PH>(p);
+        mbar_expect_tx_s(bar, kStageBytes);
+        tma3d(st, &m.tm_raw, 0, d.j, static_cast<int>(d.row16) * kRowsPerGroup, bar, pol);
+        tma3d(st + kRawStage, &m.tm_code, 0, d.j, static_cast<int>(d.row16) * kRowsPerGroup, bar, pol);
+    }
+    ++r.issued;
+}
+
+// Metadata of a stage, a lane for each tile row (row = lane % 16, tile = lane /
+// 16), as loaded words.
+struct Words {
+    uint32_t w0, w1, w2;  // version 1: base, esc_off[t], esc_off[t + 1]; version 2: tmeta[t]
+};
+
+template <int V>
+__device__ __forceinline__ Words load_words(const Mat &m, const Desc &d) {
+    const int lane = threadIdx.x & 31, t = d.j + (lane >> 4);
+    Words w = {0u, 0u, 0u};
+    if (d.live && t < m.T) {
+        const size_t at = (static_cast<size_t>(d.row16) * kRowsPerGroup + (lane & 15)) * m.T + t;
+        if (V == 1) {
+            w.w0 = __ldg(static_cast<const uint8_t *>(m.meta) + at);
+            w.w1 = __ldg(m.off + at);
+            w.w2 = __ldg(m.off + at + 1);
+        } else {
+            w.w0 = __ldg(static_cast<const uint16_t *>(m.meta) + at);
+        }
+    }
+    return w;
+}
+
+// The products of one stage: the decoded weights of each 16-column chunk and
+// its index go to `multiply`; `refill` is called once the stage's bytes are in
+// registers.
+template <int V, class Multiply, class Refill>
+__device__ __forceinline__ void stage_products(const Params &p, const Mat &m, const Desc &d, const Words &wd,
+                                               uint32_t st, Multiply multiply, Refill refill) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, tq = q >> 1, qh = q & 1;
+    const uint32_t line = static_cast<uint32_t>(2 * g + tq), rsw = line & 7u, csw = static_cast<uint32_t>(g) & 3u;
+    const uint32_t oR = st + line * 128u, oC = st + kRawStage + line * 64u;
+    const uint32_t own = V == 1 ? wd.w0 : wd.w0 & 0xFFu;
+    if (p.err && own > static_cast<uint32_t>(kMaxBase)) raise_flag(p.err, S12_FLAG_BASE);
+    const int src = tq * 16 + g;  // the lane with the words of row g's tile; row g + 8: 8 lanes on
+    const uint32_t B2A = __shfl_sync(0xFFFFFFFFu, own, src) * 0x00800080u;
+    const uint32_t B2B = __shfl_sync(0xFFFFFFFFu, own, src + 8) * 0x00800080u;
+    const bool anyesc = __any_sync(0xFFFFFFFFu, V == 1 ? wd.w1 != wd.w2 : wd.w0 >> 8 != 0u);
+    if (!anyesc) {
+        const uint4 cA0 = lds128(oC + (((2u * qh) ^ csw) << 4)), cA1 = lds128(oC + (((2u * qh + 1u) ^ csw) << 4));
+        const uint4 cB0 = lds128(oC + (((2u * qh) ^ csw) << 4) + 1024);
+        const uint4 cB1 = lds128(oC + (((2u * qh + 1u) ^ csw) << 4) + 1024);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 rA = lds128(oR + (((4u * qh + c) ^ rsw) << 4));
+            const uint4 rB = lds128(oR + (((4u * qh + c) ^ rsw) << 4) + 2048);
+            if (c == 3) refill();
+            const uint4 kA = c < 2 ? cA0 : cA1, kB = c < 2 ? cB0 : cB1;
+            uint32_t wa[8], wb[8];
+            decode_pairs(rA.x, rA.y, c & 1 ? kA.z : kA.x, B2A, wa);
+            decode_pairs(rA.z, rA.w, c & 1 ? kA.w : kA.y, B2A, wa + 4);
+            decode_pairs(rB.x, rB.y, c & 1 ? kB.z : kB.x, B2B, wb);
+            decode_pairs(rB.z, rB.w, c & 1 ? kB.w : kB.y, B2B, wb + 4);
+            multiply(c, wa, wb);
+        }
+        return;
+    }
+    // some row of the stage has escapes: a compact loop.  A lane's first half of
+    // a tile row counts from the span's start, the second half back from its end.
+    uint32_t sA, eA, sB, eB;
+    if (V == 1) {
+        sA = __shfl_sync(0xFFFFFFFFu, wd.w1, src);
+        eA = __shfl_sync(0xFFFFFFFFu, wd.w2, src);
+        sB = __shfl_sync(0xFFFFFFFFu, wd.w1, src + 8);
+        eB = __shfl_sync(0xFFFFFFFFu, wd.w2, src + 8);
+    } else {
+        // row_esc and the counts of the row's earlier tiles
+        const int r = static_cast<int>(d.row16) * kRowsPerGroup + g;
+        const uint32_t n = wd.w0 >> 8;
+        sA = __ldg(m.off + r) + prefix_count_v2(m, r, d.j, q);
+        sB = __ldg(m.off + r + 8) + prefix_count_v2(m, r + 8, d.j, q);
+        const uint32_t nA = __shfl_sync(0xFFFFFFFFu, n, g), nB = __shfl_sync(0xFFFFFFFFu, n, g + 8);
+        sA += tq ? nA : 0u;
+        sB += tq ? nB : 0u;
+        eA = sA + __shfl_sync(0xFFFFFFFFu, n, src);
+        eB = sB + __shfl_sync(0xFFFFFFFFu, n, src + 8);
+    }
+    const uint32_t nA = chunk_counts(lds128(oC + (((2u * qh) ^ csw) << 4)), lds128(oC + (((2u * qh + 1u) ^ csw) << 4)));
+    const uint32_t nB = chunk_counts(lds128(oC + (((2u * qh) ^ csw) << 4) + 1024),
+                                     lds128(oC + (((2u * qh + 1u) ^ csw) << 4) + 1024));
+    const uint32_t allA = (nA * 0x01010101u) >> 24, allB = (nB * 0x01010101u) >> 24;
+    const uint32_t pairA = allA + __shfl_xor_sync(0xFFFFFFFFu, allA, 1);
+    const uint32_t pairB = allB + __shfl_xor_sync(0xFFFFFFFFu, allB, 1);
+    if (p.err && d.j + tq < m.T && qh == 0 && (pairA != eA - sA || pairB != eB - sB))
+        raise_flag(p.err, S12_FLAG_ESC_COUNT);
+    uint32_t iA = qh ? eA - allA : sA, iB = qh ? eB - allB : sB;
+    const uint32_t limA = sA <= eA ? min(eA, m.n_esc) : 0u, limB = sB <= eB ? min(eB, m.n_esc) : 0u;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        const uint4 rA = lds128(oR + (((4u * qh + c) ^ rsw) << 4));
+        const uint4 rB = lds128(oR + (((4u * qh + c) ^ rsw) << 4) + 2048);
+        const uint32_t piece = oC + (((2u * qh + (c >> 1)) ^ csw) << 4) + 8u * (c & 1);
+        const uint2 kA = lds64(piece), kB = lds64(piece + 1024);
+        uint32_t wa[8], wb[8];
+        decode_pairs(rA.x, rA.y, kA.x, B2A, wa);
+        decode_pairs(rA.z, rA.w, kA.y, B2A, wa + 4);
+        decode_pairs(rB.x, rB.y, kB.x, B2B, wb);
+        decode_pairs(rB.z, rB.w, kB.y, B2B, wb + 4);
+        const uint32_t hereA = (nA >> (8 * c)) & 0xFFu, hereB = (nB >> (8 * c)) & 0xFFu;
+        if (hereA) patch(wa, kA, iA, limA, m.esc, p.err);
+        if (hereB) patch(wb, kB, iB, limB, m.esc, p.err);
+        iA += hereA;
+        iB += hereB;
+        multiply(c, wa, wb);
+    }
+    refill();
+}
+
+// One step by one warp.  d0 and d1 are its first stages (their copies are in
+// flight).  False when a wait gave up.
+template <int V, int PH>
+__device__ __forceinline__ bool small_step(const Params &p, const SmallShared *sm, const uint8_t *x, Ring &rg,
+                                           Feed<PH> &feed, Desc d0, Desc d1) {
+    const Mat &m = mat<PH>(p);
+    const Step &st = sm->step[PH - 1];
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, tq = q >> 1, qh = q & 1;
+    const int slots = p.tokens * p.top_k, nx = PH == 1 ? p.tokens : slots;  // rows of x or h
+    const uint32_t half = static_cast<uint32_t>(nx) * 32u, chunk_bytes = 2 * half;
+    const size_t rows = static_cast<size_t>(m.G) * kRowsPerGroup;  // of an expert
+    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains of products
+    Words w0 = load_words<V>(m, d0);
+    const uint8_t *xl = nullptr;  // the lane's column of x or h
+    float *to = nullptr;          // its places of the item's sums, for pairs 2q and 2q + 1
+    int pairs = 0;
+    bool fresh = true;
+    while (d0.live) {
+        const Words w1 = load_words<V>(m, d1);
+        if (fresh) {
+            const Item at = item_at<PH>(st, d0.it);
+            const int first = sm->s.seg_first[at.seg];
+            pairs = sm->s.seg_n[at.seg];
+            // (columns past the last pair repeat it; their results are dropped)
+            const int i = first + min(g, pairs - 1);
+            xl = x + static_cast<size_t>(PH == 1 ? sm->s.token[i] : i) * 32 + qh * 16;
+            to = (PH == 1 ? p.gu : p.d) + (static_cast<size_t>(at.range) * slots + first + 2 * q) * rows +
+                 static_cast<size_t>(at.grp) * kRowsPerGroup + g;
+        }
+        const uint32_t slot = static_cast<uint32_t>(rg.consumed & 1);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_s(rg.bars + 8u * slot, static_cast<uint32_t>(rg.consumed >> 1) & 1u))) {
+            if (lane == 0) give_up(p);
+            return false;
+        }
+        const bool live = d0.j + tq < m.T;  // the lane's tile exists (else zeros from the copy)
+        const size_t at = static_cast<size_t>(d0.j + tq) * 4 * chunk_bytes;
+        const ptrdiff_t lo = PH == 2 ? p.lo - p.hi : 0;
+        Desc d2;
+        d2.live = false;
+        auto multiply = [&](int c, const uint32_t (&wa)[8], const uint32_t (&wb)[8]) {
+            uint32_t xw[8];
+            const uint8_t *src = xl + at + c * chunk_bytes;
+            load_x(xw, src, half, live);
+            chunk_mma(acc[c & 1], wa, wb, xw);
+            if (PH == 2) {
+                load_x(xw, src + lo, half, live);
+                chunk_mma(acc[c & 1], wa, wb, xw);
+            }
+        };
+        auto refill = [&]() {
+            // the stage is in registers: hand it back to the copy engine.  (It
+            // was read only, which needs no proxy fence.)
+            __syncwarp();
+            d2 = feed.next(p, sm);
+            if (d2.live) issue_at<PH>(p, rg, d2);
+        };
+        stage_products<V>(p, m, d0, w0, rg.base + slot * kStageBytes, multiply, refill);
+        ++rg.consumed;
+        fresh = d0.last;
+        if (fresh) {
+            // lane (g, q) holds rows g and g + 8 of pairs 2q and 2q + 1
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (2 * q + i < pairs) {
+                    __stcg(to + i * rows, acc[0][i] + acc[1][i]);
+                    __stcg(to + i * rows + 8, acc[0][2 + i] + acc[1][2 + i]);
+                }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
+        }
+        d0 = d1;
+        d1 = d2;
+        w0 = w1;
+    }
+    return true;
+}
+
+__device__ __forceinline__ void add4(float4 &a, const float4 &b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+}
+
+__device__ __forceinline__ float4 shfl4(const float4 &v, int from_xor) {
+    return make_float4(__shfl_xor_sync(0xFFFFFFFFu, v.x, from_xor), __shfl_xor_sync(0xFFFFFFFFu, v.y, from_xor),
+                       __shfl_xor_sync(0xFFFFFFFFu, v.z, from_xor), __shfl_xor_sync(0xFFFFFFFFu, v.w, from_xor));
+}
+
+// The 16 sums of a pair's row group over its ranges, 4 to a lane (lane & 3);
+// lanes 4 apart add every eighth range, then one another: a fixed order.
+__device__ __forceinline__ float4 sum_ranges(const float *src, size_t plane, uint32_t ranges) {
+    const int lane = threadIdx.x & 31;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t c = lane >> 2; c < ranges; c += 8)
+        add4(v, __ldcg(reinterpret_cast<const float4 *>(src + c * plane) + (lane & 3)));
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) add4(v, shfl4(v, o));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// h from the sums of step 1: a warp takes one pair's row group at a time.
+__device__ __forceinline__ void make_hidden(const Params &p, const SmallShared *sm) {
+    const int lane = threadIdx.x & 31, slots = p.tokens * p.top_k;
+    const uint32_t G = static_cast<uint32_t>(p.up.G), ranges = sm->step[0].ranges;
+    const int last = sm->s.n_segs - 1, pairs = sm->s.seg_first[last] + sm->s.seg_n[last];  // that are in use
+    const size_t rows = static_cast<size_t>(G) * kRowsPerGroup, plane = static_cast<size_t>(slots) * rows;
+    for (uint32_t u = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < pairs * G; u += gridDim.x * kWarps) {
+        const uint32_t pos = u / G, grp = u - pos * G;
+        const float4 v = sum_ranges(p.gu + pos * rows + static_cast<size_t>(grp) * kRowsPerGroup, plane, ranges);
+        // lanes 0 and 1: gate rows 0-3 and 4-7; lanes 2 and 3: the up rows
+        const float4 up = shfl4(v, 2);
+        auto h = [](float g, float t) { return g / (1.f + expf(-g)) * t; };
+        const float4 a = make_float4(h(v.x, up.x), h(v.y, up.y), h(v.z, up.z), h(v.w, up.w));
+        const float4 b = shfl4(a, 1);
+        if (lane == 0) {
+            // one piece, in the order 0 4 1 5 2 6 3 7
+            const float f[8] = {a.x, b.x, a.y, b.y, a.z, b.z, a.w, b.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hi[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+                const float r0 = f[2 * i] - __uint_as_float(hi[i] << 16);
+                const float r1 = f[2 * i + 1] - __uint_as_float(hi[i] & 0xFFFF0000u);
+                // (an infinite h has no rest)
+                lo[i] = pack_bf16(fabsf(r0) < 3.4e38f ? r0 : 0.f, fabsf(r1) < 3.4e38f ? r1 : 0.f);
+            }
+            const int in = static_cast<int>(grp & 15u);
+            const size_t o = piece_at(static_cast<int>(grp >> 4), (in >> 1) & 3, in & 1, slots, static_cast<int>(pos),
+                                      in >> 3);
+            *reinterpret_cast<uint4 *>(p.hi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(p.lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+}
+
+// y from the sums of step 2: a warp takes 16 values of a token at a time.
+__device__ __forceinline__ void make_y(const Params &p, const SmallShared *sm) {
+    const int lane = threadIdx.x & 31, slots = p.tokens * p.top_k;
+    const uint32_t G = static_cast<uint32_t>(p.down.G), ranges = sm->step[1].ranges;
+    const size_t rows = static_cast<size_t>(G) * kRowsPerGroup, plane = static_cast<size_t>(slots) * rows;
+    for (uint32_t u = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < p.tokens * G; u += gridDim.x * kWarps) {
+        const uint32_t t = u / G, grp = u - t * G;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < p.top_k; ++s) {
+            const int i = static_cast<int>(t) * p.top_k + s;
+            if (sm->s.expert[i] < 0) continue;
+            const float4 v = sum_ranges(p.d + sm->s.place[i] * rows + static_cast<size_t>(grp) * kRowsPerGroup, plane,
+                                        ranges);
+            const float w = sm->s.weight[i];
+            y = make_float4(fmaf(w, v.x, y.x), fmaf(w, v.y, y.y), fmaf(w, v.z, y.z), fmaf(w, v.w, y.w));
+        }
+        if (lane < 4) {
+            const size_t o = static_cast<size_t>(t) * p.H + static_cast<size_t>(grp) * kRowsPerGroup + 4 * lane;
+            put_y(p, o, y.x);
+            put_y(p, o + 1, y.y);
+            put_y(p, o + 2, y.z);
+            put_y(p, o + 3, y.w);
+        }
+    }
+}
+
+template <int V>
+__global__ void __launch_bounds__(kThreads, 1) moe_small_kernel(const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    SmallShared *sm = reinterpret_cast<SmallShared *>(base + kRingBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Ring rg;
+    rg.bars = smem_addr(sm->s.bars) + static_cast<uint32_t>(warp) * kStages * 8u;
+    rg.base = smem_addr(base) + static_cast<uint32_t>(warp) * kStages * kStageBytes;
+    rg.issued = rg.consumed = 0;
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init_s(rg.bars + 8u * s, 1);
+        fence_barrier_init();
+    }
+    // x and the scores: a few tokens by every CTA for itself (x behind the
+    // lists, the scores where the ring will be), more by the grid
+    const uint8_t *x = p.xp;
+    const double *scores = p.scores;
+    bool ok = true;
+    if (p.local) {
+        uint8_t *xs = base + kRingBytes + ((sizeof(SmallShared) + 15) & ~size_t(15));
+        double *own = reinterpret_cast<double *>(base);
+        pack_x(p, xs, threadIdx.x, kThreads);
+        if (!p.ids_in) score<1, 1>(p, own, warp, kWarps);
+        x = xs;
+        scores = own;
         __syncthreads();
-        if (threadIdx.x < kSyncWords) p.sync[threadIdx.x] = 0u;
+    } else {
+        pack_x(p, p.xp, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
+        if (!p.ids_in) {
+            const int u0 = warp * gridDim.x + blockIdx.x, step = gridDim.x * kWarps;
+            if (p.tokens >= 8 && p.tokens * p.experts >= 1024)
+                score<4, 4>(p, p.scores, u0, step);
+            else
+                score<1, 1>(p, p.scores, u0, step);
+        }
+        ok = grid_meet(p, &sm->s, kBarRoute);
     }
+    if (ok) {
+        route(p, &sm->s, scores);
+        if (sm->s.n_segs == 0) {
+            // no token goes anywhere
+            const size_t n = static_cast<size_t>(p.tokens) * p.H;
+            for (size_t i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) put_y(p, i, 0.f);
+        } else {
+            if (threadIdx.x == 0) plan_step<1>(p, sm);
+            if (threadIdx.x == 32) plan_step<2>(p, sm);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scores give way to copies
+            __syncthreads();
+            Feed<1> f1;
+            f1.start(p, sm);
+            Desc d0 = f1.next(p, sm);
+            if (d0.live) issue_at<1>(p, rg, d0);
+            Desc d1 = f1.next(p, sm);
+            if (d1.live) issue_at<1>(p, rg, d1);
+            ok = small_step<V, 1>(p, sm, x, rg, f1, d0, d1);
+            // the first copies of step 2 run while the grid meets
+            Feed<2> f2;
+            f2.start(p, sm);
+            if (ok) {
+                d0 = f2.next(p, sm);
+                if (d0.live) issue_at<2>(p, rg, d0);
+                d1 = f2.next(p, sm);
+                if (d1.live) issue_at<2>(p, rg, d1);
+            }
+            if (grid_meet(p, &sm->s, kBarSums)) {
+                make_hidden(p, sm);
+                if (grid_meet(p, &sm->s, kBarHidden)) {
+                    if (ok) small_step<V, 2>(p, sm, p.hi, rg, f2, d0, d1);
+                    if (grid_meet(p, &sm->s, kBarDown)) make_y(p, sm);
+                }
+            }
+        }
+    }
+    finish(p, &sm->s, rg);
 }
 
 }  // namespace moe
@@ -993,8 +1494,11 @@ constexpr uint32_t kSmemLimit = 227 * 1024;
 
 struct MoePlan {
     int sms, segs, nt;
+    bool small, local;
+    int seg;
+    uint32_t range_up, range_down, smem;
     uint64_t n_cnt, cnt_down, cnt_y;
-    size_t sync, cnt, scores, xp, hi, lo, d, warp_part, cta_part, total;
+    size_t sync, cnt, scores, xp, hi, lo, gu, d, warp_part, cta_part, total;
 };
 
 // Workspace parts; the words that have to be zero between calls come first.
@@ -1005,12 +1509,24 @@ MoePlan plan(const MoeCall &c, int sms) {
     pl.sms = sms;
     // (not by this call's tokens: the counters then lie in the same place for
     // every call with these containers, and what another call left there is zero)
-    pl.segs = c.experts + moe::kMaxSlots / moe::kSeg;
+    pl.segs = c.experts + moe::kMaxSlots / moe::kSegSmall;
+    // few pairs an expert on average: warps share a row group's columns (one
+    // with more than eight pairs is read once for every eight)
+    pl.small = slots <= 4ull * c.experts || c.tokens <= 8;
+    pl.seg = pl.small ? moe::kSegSmall : moe::kSegLarge;
+    const uint32_t fixed = 1024 + moe::kRingBytes + align_up(sizeof(moe::SmallShared), 16);
+    const uint64_t x_bytes = 2ull * c.tokens * H;
+    // little enough for every CTA to do alone: less time than a meeting of the grid
+    pl.local = pl.small && fixed + x_bytes <= kSmemLimit && c.tokens * c.experts <= 512 &&
+               (c.ids_in || static_cast<uint64_t>(c.tokens) * c.experts * H <= (1u << 18));
+    pl.smem = pl.small ? fixed + static_cast<uint32_t>(pl.local ? x_bytes : 0)
+                       : 1024 + moe::kRingBytes + moe::kWarps * 2 * moe::kPartBytes + sizeof(moe::Shared);
+    pl.range_up = pl.range_down = 4;
     const uint64_t g_up = 2 * F / 16, g_down = H / 16;
     pl.cnt_down = pl.segs * g_up;
     pl.cnt_y = pl.cnt_down + pl.segs * g_down;
     pl.n_cnt = pl.cnt_y + g_down;
-    const int most = static_cast<int>(std::min<uint64_t>(slots, moe::kSeg));
+    const int most = static_cast<int>(std::min<uint64_t>(slots, pl.seg));  // pairs of a segment
     pl.nt = most <= 8 ? 1 : most <= 16 ? 2 : most <= 32 ? 4 : 8;
     size_t at = 0;
     auto take = [&](uint64_t bytes) {
@@ -1024,7 +1540,11 @@ MoePlan plan(const MoeCall &c, int sms) {
     pl.xp = take(2ull * c.tokens * H);
     pl.hi = take(2 * slots * F);
     pl.lo = take(2 * slots * F);
-    pl.d = take(4 * slots * H);
+    const auto ranges = [&](uint64_t cols, uint32_t stages) {
+        return pl.small ? ((cols / kTile + stage::kNT - 1) / stage::kNT + stages - 1) / stages : 1;
+    };
+    pl.gu = take(pl.small ? 4 * slots * 2 * F * ranges(H, pl.range_up) : 0);
+    pl.d = take(4 * slots * H * ranges(F, pl.range_down));
     pl.warp_part = take(pl.nt == 1 ? 0 : static_cast<uint64_t>(sms) * moe::kWarps * 2 * pl.nt * moe::kPartBytes);
     pl.cta_part = take(static_cast<uint64_t>(sms) * 2 * pl.nt * moe::kPartBytes);
     pl.total = at;
@@ -1089,13 +1609,17 @@ int launch_moe(const MoeCall &c, void *ws, size_t ws_bytes, cudaStream_t stream)
     p.xp = w + pl.xp;
     p.hi = w + pl.hi;
     p.lo = w + pl.lo;
+    p.gu = reinterpret_cast<float *>(w + pl.gu);
     p.d = reinterpret_cast<float *>(w + pl.d);
     p.warp_part = reinterpret_cast<float *>(w + pl.warp_part);
     p.cta_part = reinterpret_cast<float *>(w + pl.cta_part);
-    const uint32_t smem = 1024 + moe::kRingBytes + moe::kWarps * 2 * moe::kPartBytes + sizeof(moe::Shared);
-    static_assert(1024 + moe::kRingBytes + moe::kWarps * 2 * moe::kPartBytes + sizeof(moe::Shared) <= kSmemLimit,
-                  "the rings, parts and lists fit one SM");
-    auto kern = c.up->version == 1 ? moe::moe_kernel<1> : moe::moe_kernel<2>;
+    p.local = pl.local;
+    p.seg = pl.seg;
+    p.range_up = pl.range_up;
+    p.range_down = pl.range_down;
+    const uint32_t smem = pl.smem;
+    auto kern = pl.small ? (c.up->version == 1 ? moe::moe_small_kernel<1> : moe::moe_small_kernel<2>)
+                         : (c.up->version == 1 ? moe::moe_kernel<1> : moe::moe_kernel<2>);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return S12_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
