@@ -427,30 +427,51 @@ def s12_gemm_skinny_bf16(view: View, x: torch.Tensor, y: torch.Tensor | None = N
     return y
 
 
-def _on_current_device(*tensors):
-    """The library's pointers belong to the current device: refuse tensors
-    of another one (their addresses would be used there)."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"expected tensors on the current device (cuda:{dev}), got {t.device}")
+# The calls below take a few microseconds on the device, so their checks are
+# kept short: one pass over each tensor, and no object made for a pointer.
+
+def _here(t: torch.Tensor | None, dev: int):
+    """The address of a contiguous tensor of the current device (the one the
+    library's pointers belong to)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"expected a tensor on the current device (cuda:{dev}), got one on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev: int):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+_BITS16 = (torch.int16, torch.bfloat16, torch.uint16)
+_VALUES = (torch.float32,) + _BITS16
 
 
 def _value_type(t: torch.Tensor) -> int:
     """S12_TYPE_* of a tensor: FP32, or BF16 (also as 16-bit patterns)."""
     if t.dtype is torch.float32:
         return S12_TYPE_F32
-    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+    if t.dtype in _BITS16:
         return S12_TYPE_BF16
     raise TypeError(f"expected a BF16 (or 16-bit pattern) or FP32 tensor, got {t.dtype}")
 
 
 def _expect(t: torch.Tensor, shape, dtypes, name: str):
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+    if t.shape != shape or t.dtype not in dtypes:
         raise ValueError(f"{name}: expected {tuple(shape)} of {dtypes}, got {tuple(t.shape)} of {t.dtype}")
 
 
-_BITS16 = (torch.int16, torch.bfloat16, torch.uint16)
+def _or_empty(t: torch.Tensor | None, like: torch.Tensor, shape, dtype, dtypes, name: str) -> torch.Tensor:
+    """An output: the tensor that is given, checked, or a new one."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    _expect(t, shape, dtypes, name)
+    return t
 
 
 def s12_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
@@ -464,57 +485,48 @@ def s12_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
     where `int8`; None for what was not asked for."""
     if not (bf16 or int8):
         raise ValueError("nothing to compute: neither bf16 nor int8")
-    cols = x.shape[-1]
+    shape = x.shape
+    cols = shape[-1]
     rows = x.numel() // cols if cols else 0
+    rt = S12_TYPE_BF16
     if residual is not None:
-        _expect(residual, x.shape, (torch.float32,) + _BITS16, "residual")
+        rt = _value_type(residual)
+        _expect(residual, shape, _VALUES, "residual")
         if residual_out is None:
             residual_out = residual
-    rt = S12_TYPE_BF16
-    if residual_out is not None:
-        rt = _value_type(residual_out)
-        _expect(residual_out, x.shape, (torch.float32,) + _BITS16, "residual_out")
-        if residual is not None and _value_type(residual) != rt:
+    if residual_out is not None and residual_out is not residual:
+        ot = _value_type(residual_out)
+        _expect(residual_out, shape, _VALUES, "residual_out")
+        if residual is not None and rt != ot:
             raise ValueError("residual and residual_out must have the same type")
+        rt = ot
     if weight is not None:
         _expect(weight, (cols,), _BITS16, "weight")
-    if bf16:
-        if y is None:
-            y = torch.empty(x.shape, dtype=torch.int16, device=x.device)
-        else:
-            _expect(y, x.shape, _BITS16, "y")
-    if int8:
-        if q is None:
-            q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-        else:
-            _expect(q, x.shape, (torch.int8,), "q")
-        if scale is None:
-            scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        else:
-            _expect(scale, x.shape[:-1], (torch.float32,), "scale")
-    y, q, scale = (y if bf16 else None), (q if int8 else None), (scale if int8 else None)
-    _on_current_device(x, weight, residual, residual_out, y, q, scale)
-    _check(_lib().s12_rmsnorm(_dptr(x), _value_type(x), _dptr(residual), _dptr(residual_out), rt, _dptr(weight), rows,
-                              cols, eps, _dptr(y), _dptr(q), _dptr(scale), _stream(stream)), "s12_rmsnorm")
+    y = _or_empty(y, x, shape, torch.int16, _BITS16, "y") if bf16 else None
+    q = _or_empty(q, x, shape, torch.int8, (torch.int8,), "q") if int8 else None
+    scale = _or_empty(scale, x, shape[:-1], torch.float32, (torch.float32,), "scale") if int8 else None
+    dev = torch.cuda.current_device()
+    rc = _lib().s12_rmsnorm(_here(x, dev), _value_type(x), _here(residual, dev), _here(residual_out, dev), rt,
+                            _here(weight, dev), rows, cols, eps, _here(y, dev), _here(q, dev), _here(scale, dev),
+                            _raw_stream(stream, dev))
+    if rc:
+        raise S12Error(rc, "s12_rmsnorm")
     return y, q, scale, residual_out
 
 
 def s12_quant_i8(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
     """(q, scale): the rows of x (BF16 or FP32, along its last dimension) as
     int8 with one FP32 scale a row."""
-    cols = x.shape[-1]
+    shape = x.shape
+    cols = shape[-1]
     rows = x.numel() // cols if cols else 0
-    if q is None:
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-    else:
-        _expect(q, x.shape, (torch.int8,), "q")
-    if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    else:
-        _expect(scale, x.shape[:-1], (torch.float32,), "scale")
-    _on_current_device(x, q, scale)
-    _check(_lib().s12_quant_i8(_dptr(x), _value_type(x), rows, cols, _dptr(q), _dptr(scale), _stream(stream)),
-           "s12_quant_i8")
+    q = _or_empty(q, x, shape, torch.int8, (torch.int8,), "q")
+    scale = _or_empty(scale, x, shape[:-1], torch.float32, (torch.float32,), "scale")
+    dev = torch.cuda.current_device()
+    rc = _lib().s12_quant_i8(_here(x, dev), _value_type(x), rows, cols, _here(q, dev), _here(scale, dev),
+                             _raw_stream(stream, dev))
+    if rc:
+        raise S12Error(rc, "s12_quant_i8")
     return q, scale
 
 
@@ -535,19 +547,20 @@ def s12_gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     BF16 bits (or FP32 where `f32`, or in the type of the y that is given)."""
     M, K = x.shape
     N = w.shape[0]
-    _expect(x, (M, K), (torch.int8,), "x")
+    if x.dtype is not torch.int8:
+        raise ValueError(f"x: expected int8, got {x.dtype}")
     _expect(w, (N, K), (torch.int8,), "w")
     _expect(x_scale, (M,), (torch.float32,), "x_scale")
     _expect(w_scale, (N,), (torch.float32,), "w_scale")
-    if y is None:
-        y = torch.empty((M, N), dtype=torch.float32 if f32 else torch.int16, device=x.device)
-    else:
-        _expect(y, (M, N), (torch.float32,) + _BITS16, "y")
+    y = _or_empty(y, x, (M, N), torch.float32 if f32 else torch.int16, _VALUES, "y")
     if ws is None:
         ws = gemm_i8_workspace(M, device=x.device)
-    _on_current_device(x, x_scale, w, w_scale, y, ws, err_flag)
-    _check(_lib().s12_gemm_i8(_dptr(x), _dptr(x_scale), _dptr(w), _dptr(w_scale), M, N, K, _dptr(y), _value_type(y),
-                              _dptr(ws), ws.numel(), _dptr(err_flag), _stream(stream)), "s12_gemm_i8")
+    dev = torch.cuda.current_device()
+    rc = _lib().s12_gemm_i8(_here(x, dev), _here(x_scale, dev), _here(w, dev), _here(w_scale, dev), M, N, K,
+                            _here(y, dev), _value_type(y), _here(ws, dev), ws.numel() * ws.element_size(),
+                            _here(err_flag, dev), _raw_stream(stream, dev))
+    if rc:
+        raise S12Error(rc, "s12_gemm_i8")
     return y
 
 
@@ -563,13 +576,10 @@ def moe_workspace(gate_up: View, down: View, experts: int, tokens: int, top_k: i
 
 
 def _moe_io(down: View, x: torch.Tensor, experts: int, y, f32: bool):
-    hidden = int(down.rows) // max(experts, 1)
+    hidden = down.rows // max(experts, 1)
     if x.dim() != 2 or x.shape[1] != hidden or x.dtype not in _BITS16:
         raise ValueError(f"x: expected (tokens, {hidden}) of 16-bit values, got {tuple(x.shape)} of {x.dtype}")
-    if y is None:
-        return torch.empty(x.shape, dtype=torch.float32 if f32 else torch.int16, device=x.device)
-    _expect(y, x.shape, (torch.float32,) + _BITS16, "y")
-    return y
+    return _or_empty(y, x, x.shape, torch.float32 if f32 else torch.int16, _VALUES, "y")
 
 
 def s12_moe(gate_up: View, down: View, experts: int, x: torch.Tensor, router: torch.Tensor, top_k: int,
@@ -584,20 +594,17 @@ def s12_moe(gate_up: View, down: View, experts: int, x: torch.Tensor, router: to
     y = _moe_io(down, x, experts, y, f32)
     T = x.shape[0]
     _expect(router, (experts, x.shape[1]), _BITS16, "router")
-    if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
-    else:
-        _expect(ids, (T, top_k), (torch.int32,), "ids")
-    if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
-    else:
-        _expect(weights, (T, top_k), (torch.float32,), "weights")
+    ids = _or_empty(ids, x, (T, top_k), torch.int32, (torch.int32,), "ids")
+    weights = _or_empty(weights, x, (T, top_k), torch.float32, (torch.float32,), "weights")
     if ws is None:
         ws = moe_workspace(gate_up, down, experts, T, top_k, x.device)
-    _on_current_device(x, router, y, ids, weights, ws, err_flag)
-    _check(_lib().s12_moe(C.byref(gate_up), C.byref(down), experts, _dptr(x), T, _dptr(router), top_k, int(renorm),
-                          _dptr(y), _value_type(y), _dptr(ids), _dptr(weights), _dptr(ws), ws.numel(),
-                          _dptr(err_flag), _stream(stream)), "s12_moe")
+    dev = torch.cuda.current_device()
+    rc = _lib().s12_moe(C.byref(gate_up), C.byref(down), experts, _here(x, dev), T, _here(router, dev), top_k,
+                        int(renorm), _here(y, dev), _value_type(y), _here(ids, dev), _here(weights, dev),
+                        _here(ws, dev), ws.numel() * ws.element_size(), _here(err_flag, dev),
+                        _raw_stream(stream, dev))
+    if rc:
+        raise S12Error(rc, "s12_moe")
     return y, ids, weights
 
 
@@ -610,15 +617,17 @@ def s12_moe_routed(gate_up: View, down: View, experts: int, x: torch.Tensor, ids
     T = x.shape[0]
     if ids.dim() != 2:
         raise ValueError("ids must be tokens x top_k")
-    _expect(ids, (T, ids.shape[1]), (torch.int32,), "ids")
-    _expect(weights, tuple(ids.shape), (torch.float32,), "weights")
     top_k = ids.shape[1]
+    _expect(ids, (T, top_k), (torch.int32,), "ids")
+    _expect(weights, (T, top_k), (torch.float32,), "weights")
     if ws is None:
         ws = moe_workspace(gate_up, down, experts, T, top_k, x.device)
-    _on_current_device(x, ids, weights, y, ws, err_flag)
-    _check(_lib().s12_moe_routed(C.byref(gate_up), C.byref(down), experts, _dptr(x), T, _dptr(ids), _dptr(weights),
-                                 top_k, _dptr(y), _value_type(y), _dptr(ws), ws.numel(), _dptr(err_flag),
-                                 _stream(stream)), "s12_moe_routed")
+    dev = torch.cuda.current_device()
+    rc = _lib().s12_moe_routed(C.byref(gate_up), C.byref(down), experts, _here(x, dev), T, _here(ids, dev),
+                               _here(weights, dev), top_k, _here(y, dev), _value_type(y), _here(ws, dev),
+                               ws.numel() * ws.element_size(), _here(err_flag, dev), _raw_stream(stream, dev))
+    if rc:
+        raise S12Error(rc, "s12_moe_routed")
     return y
 
 
