@@ -12,14 +12,13 @@
 // that a weight costs few instructions.
 //
 // Steps, by one cooperative grid of one CTA per SM:
-//   0. x is rewritten in the order the products read it; the scores are
-//      summed; grid barrier; every CTA selects the experts and sorts the
-//      (token, slot) pairs by expert by itself.
-//   1. gate/up products and the SwiGLU, into the workspace (h).
-//   2. grid barrier; down products (d); the last of a row group's experts adds
-//      them by token, in slot order, and stores y.
-// The first copies of step 2 are issued before the barrier: weights do not
-// depend on it, so the copy engines run on while the grid meets.
+//   0. x is rewritten in the order the products read it; scores; every CTA
+//      selects the experts and sorts the (token, slot) pairs by expert itself.
+//   1. gate/up products; their sums go to the workspace by ranges of columns.
+//      The grid meets, adds the ranges, applies the SwiGLU, and meets again.
+//   2. down products, sums by ranges; the grid meets and adds ranges and slots.
+// The first copies of step 2 are issued before the grid meets: weights do not
+// depend on it.
 //
 // Products.  As in the GEMV, a warp takes 16 rows x 2 tiles of weights a stage
 // from its own ring of two, decodes them in registers into the A operand of
@@ -33,16 +32,16 @@
 // pairs in a register.  h is kept as the sum of two BF16 values, so that it
 // carries 16 bits of mantissa and y is rounded once, where it is stored.
 //
-// Work split (stream-K).  The stages of all active experts are numbered row
-// group after row group and dealt to the grid's warps in equal ranges.  A row
-// group that several warps share is added up as in the GEMV: through the
-// CTA's parts, and across CTAs by the last to arrive.  All sums have a fixed
-// order, so y is the same on every call.
+// Two kernels share these steps.  With few pairs an expert (4 on average, or at
+// most 8 tokens) x comes through L1 and warps take items one by one; with more
+// the warps of a CTA go through the same columns side by side, and x comes
+// through shared memory once for all of them.
 //
-// Every wait is bounded.  One that gives up raises S12_FLAG_TIMEOUT and a word
-// that the other waits watch; the CTAs then leave, and the last one clears
-// the counters.
+// All sums have a fixed order, so y is the same on every call.  Every wait is
+// bounded.  One that gives up raises S12_FLAG_TIMEOUT and a word that the other
+// waits watch; the CTAs then leave, and the last one clears the words.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -55,14 +54,17 @@ namespace moe {
 
 using namespace stage;
 
-constexpr int kWarps = 16;   // warps per CTA, one CTA per SM
+constexpr int kWarps = 16;   // warps per CTA of the kernel for few pairs, one CTA per SM
 constexpr int kThreads = 32 * kWarps;
+constexpr int kLargeWarps = 12;  // and of the one for many, beside one that copies x
+constexpr int kLargeThreads = 32 * (kLargeWarps + 1);
 constexpr int kStages = 2;   // stages per warp ring
+constexpr int kAhead = 3;    // units that a CTA of the kernel for many knows in advance
 constexpr int kSegSmall = 8, kSegLarge = 64;  // (token, slot) pairs that share one read of an expert's weights
 constexpr int kMaxSlots = S12_MOE_MAX_TOKENS * S12_MOE_MAX_TOP_K;
 constexpr int kMaxSegs = S12_MOE_MAX_EXPERTS + kMaxSlots / kSegSmall;
-constexpr uint32_t kPartBytes = 512;  // one warp's sums of 16 rows x 8 tokens
 constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
+constexpr uint32_t kLargeRingBytes = kLargeWarps * kStages * kStageBytes;
 
 // A matrix of all experts: expert after expert, rows_e rows each.
 struct __align__(64) Mat {
@@ -78,7 +80,7 @@ struct __align__(64) Mat {
 };
 
 // Words that the grid meets at.
-enum { kBarRoute, kBarSums, kBarHidden, kBarDown, kNext1, kNext2, kExits, kAbort, kSyncWords };
+enum { kBarRoute, kBarPack, kBarSums, kBarHidden, kBarDown, kNext1, kNext2, kExits, kAbort, kSyncWords };
 
 struct __align__(64) Params {
     Mat up, down;
@@ -92,19 +94,14 @@ struct __align__(64) Params {
     int tokens, experts, top_k, H, F;
     int renorm, y_f32;
     int seg;         // pairs of a segment at most
-    // the kernel for few tokens:
-    int local;       // every CTA routes for itself, with x in shared memory
-    uint32_t range_up, range_down;  // stages of an item
+    int local;       // few pairs: every CTA routes for itself, with x in shared memory
+    uint32_t range;  // stages of an item
+    uint32_t pool;   // many pairs: bytes of shared memory for x
     // workspace
-    uint32_t *sync;         // kSyncWords
-    uint32_t *cnt;          // arrivals: [segs][G up], [segs][G down], [G down]
-    uint32_t n_cnt, cnt_down, cnt_y;
+    uint32_t *sync;         // kSyncWords, zero between calls
     double *scores;         // [tokens][experts]
     uint8_t *xp, *hi, *lo;  // x, and h as two BF16 values, in the products' order
-    float *gu;              // few tokens: [ranges][slots][2F]
-    float *d;               // [slots][H], few tokens: [ranges][slots][H]
-    float *warp_part;       // [CTAs * kWarps][2][NT][128] for more than 8 tokens an expert
-    float *cta_part;        // [CTAs][2][NT][128]
+    float *gu, *d;          // sums of the two steps: [ranges][slots][2F], [ranges][slots][H]
 };
 
 struct Shared {
@@ -114,6 +111,7 @@ struct Shared {
     uint16_t list[kMaxSlots];   // (token, slot) pairs by expert
     uint16_t token[kMaxSlots];  // of each of them
     uint16_t place[kMaxSlots];  // of each (token, slot) in the list
+    uint16_t segment[kMaxSlots];  // of each of the list
     int count[S12_MOE_MAX_EXPERTS], first[S12_MOE_MAX_EXPERTS];
     uint16_t seg_expert[kMaxSegs], seg_first[kMaxSegs];
     uint8_t seg_n[kMaxSegs];
@@ -121,11 +119,11 @@ struct Shared {
     int ok, last;
 };
 
-// Order of x and h in the workspace, in 16-byte pieces of 8 values: tile,
-// then 16-column chunk of a lane's 64, then half chunk, then token (of x) or
-// sorted pair (of h), then which 64 columns of the tile.  A warp's load of
-// one half chunk is then contiguous over tokens.  Inside a piece the values
-// come as 0 4 1 5 2 6 3 7.
+// Order of x and h, in 16-byte pieces of 8 values: tile, then 16-column chunk of
+// a lane's 64, then half chunk, then which of n tokens or pairs, then which 64
+// columns of the tile.  A warp's load of one half chunk is then contiguous over
+// them.  h (and x, where many pairs share an expert) comes segment by segment.
+// Inside a piece the values come as 0 4 1 5 2 6 3 7.
 __device__ __forceinline__ size_t piece_at(int tile, int chunk, int half, int n, int i, int qh) {
     return ((((static_cast<size_t>(tile) * 4 + chunk) * 2 + half) * n + i) * 2 + qh) * 16;
 }
@@ -173,16 +171,31 @@ __device__ __forceinline__ bool grid_meet(const Params &p, Shared *sm, int word)
 // ---------------------------------------------------------------------------
 // Step 0: x in the products' order, scores, experts.
 
+// Piece c8 of token t, to place i of n.
+__device__ __forceinline__ void pack_piece(const Params &p, uint8_t *to, int t, int c8, int n, int i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(t) * p.H) + c8);
+    const int in = c8 & 15;  // piece of the tile: 64 columns, chunk, half
+    uint4 *dst = reinterpret_cast<uint4 *>(to + piece_at(c8 >> 4, (in >> 1) & 3, in & 1, n, i, in >> 3));
+    *dst = make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u),
+                      prmt(v.y, v.w, 0x7632u));
+}
+
+// x token by token.
 __device__ __forceinline__ void pack_x(const Params &p, uint8_t *to, int i0, int step) {
     const int per_row = p.H / 8;
     const int n = p.tokens * per_row;
     for (int i = i0; i < n; i += step) {
         const int t = i / per_row, c8 = i - t * per_row;  // piece c8 of token t
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.x) + i);
-        const int in = c8 & 15;  // piece of the tile: 64 columns, chunk, half
-        uint4 *dst = reinterpret_cast<uint4 *>(to + piece_at(c8 >> 4, (in >> 1) & 3, in & 1, p.tokens, t, in >> 3));
-        *dst = make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u),
-                          prmt(v.y, v.w, 0x7632u));
+        pack_piece(p, to, t, c8, p.tokens, t);
+    }
+}
+
+// x segment by segment, a copy for each pair.
+__device__ __forceinline__ void pack_sorted(const Params &p, const Shared *sm, int pairs) {
+    const int per_row = p.H / 8;
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < pairs * per_row; i += gridDim.x * blockDim.x) {
+        const int at = i / per_row, c8 = i - at * per_row, seg = sm->segment[at], first = sm->seg_first[seg];
+        pack_piece(p, p.xp + static_cast<size_t>(first) * p.H * 2, sm->token[at], c8, sm->seg_n[seg], at - first);
     }
 }
 
@@ -318,13 +331,13 @@ __device__ __forceinline__ void select_experts(const Params &p, Shared *sm, cons
 __device__ __forceinline__ void route(const Params &p, Shared *sm, const double *scores) {
     const int slots = p.tokens * p.top_k, tid = threadIdx.x;
     if (p.ids_in) {
-        if (tid < slots) {
-            const int e = __ldg(p.ids_in + tid);
-            sm->expert[tid] = static_cast<int16_t>(e >= 0 && e < p.experts ? e : -1);
-            sm->weight[tid] = __ldg(p.weights_in + tid);
+        for (int i = tid; i < slots; i += blockDim.x) {
+            const int e = __ldg(p.ids_in + i);
+            sm->expert[i] = static_cast<int16_t>(e >= 0 && e < p.experts ? e : -1);
+            sm->weight[i] = __ldg(p.weights_in + i);
         }
     } else {
-        for (int t = tid >> 5; t < p.tokens; t += kWarps) select_experts(p, sm, scores, t);
+        for (int t = tid >> 5; t < p.tokens; t += blockDim.x >> 5) select_experts(p, sm, scores, t);
     }
     __syncthreads();
     if (tid < p.experts) {
@@ -355,7 +368,10 @@ __device__ __forceinline__ void route(const Params &p, Shared *sm, const double 
         int at = pairs_to - pairs, seg = segs_to - segs;
         for (int i = 0; i < kPer; ++i) {
             const int e = tid * kPer + i, n = e < p.experts ? sm->count[e] : 0;
-            if (e < p.experts) sm->first[e] = at;
+            if (e < p.experts) {
+                sm->first[e] = at;
+                sm->count[e] = n ? seg : -1;  // (from here on the expert's first segment)
+            }
             for (int k = 0; k < n; k += p.seg, ++seg) {
                 sm->seg_expert[seg] = static_cast<uint16_t>(e);
                 sm->seg_first[seg] = static_cast<uint16_t>(at + k);
@@ -370,10 +386,12 @@ __device__ __forceinline__ void route(const Params &p, Shared *sm, const double 
         }
     }
     __syncthreads();
-    if (tid < p.experts && sm->count[tid]) {
-        int at = sm->first[tid];
+    if (tid < p.experts && sm->count[tid] >= 0) {
+        const int first = sm->first[tid], seg = sm->count[tid];
+        int at = first;
         for (int i = 0; i < slots; ++i)
             if (sm->expert[i] == tid) {
+                sm->segment[at] = static_cast<uint16_t>(seg + (at - first) / p.seg);
                 sm->place[i] = static_cast<uint16_t>(at);
                 sm->token[at] = static_cast<uint16_t>(i / p.top_k);
                 sm->list[at++] = static_cast<uint16_t>(i);
@@ -382,61 +400,9 @@ __device__ __forceinline__ void route(const Params &p, Shared *sm, const double 
     __syncthreads();
 }
 
-// ---------------------------------------------------------------------------
-// Positions.  PH 1: row groups by segment, then row; PH 2: by row, then
-// segment (all of a row's experts end close together).
-
 template <int PH>
 __device__ __forceinline__ const Mat &mat(const Params &p) {
     return PH == 1 ? p.up : p.down;
-}
-
-template <int PH>
-__device__ __forceinline__ void split(const Params &p, const Shared *sm, uint32_t gi, uint32_t &seg, uint32_t &grp) {
-    if (PH == 1) {
-        seg = gi / static_cast<uint32_t>(p.up.G);
-        grp = gi - seg * static_cast<uint32_t>(p.up.G);
-    } else {
-        grp = gi / static_cast<uint32_t>(sm->n_segs);
-        seg = gi - grp * static_cast<uint32_t>(sm->n_segs);
-    }
-}
-
-// A stage: row group gi of the step, first tile j, `left` stages of the
-// warp's range from here on; row16: its 16-row group in the matrix.
-struct Cur {
-    uint32_t gi;
-    int j, left;
-    uint32_t row16;
-};
-
-template <int PH>
-__device__ __forceinline__ uint32_t row16_of(const Params &p, const Shared *sm, uint32_t gi) {
-    uint32_t seg, grp;
-    split<PH>(p, sm, gi, seg, grp);
-    return sm->seg_expert[seg] * static_cast<uint32_t>(mat<PH>(p).G) + grp;
-}
-
-template <int PH>
-__device__ __forceinline__ Cur locate(const Params &p, const Shared *sm, uint32_t s, int left) {
-    const uint32_t S = mat<PH>(p).S;
-    Cur c;
-    c.gi = s / S;
-    c.j = static_cast<int>(s - c.gi * S) * kNT;
-    c.left = left;
-    c.row16 = left > 0 ? row16_of<PH>(p, sm, c.gi) : 0u;
-    return c;
-}
-
-template <int PH>
-__device__ __forceinline__ void advance(const Params &p, const Shared *sm, Cur &c) {
-    --c.left;
-    c.j += kNT;
-    if (c.j >= mat<PH>(p).T) {
-        c.j = 0;
-        ++c.gi;
-        if (c.left > 0) c.row16 = row16_of<PH>(p, sm, c.gi);
-    }
 }
 
 // The warp's ring: stages issued and consumed so far, over both steps.
@@ -445,23 +411,8 @@ struct Ring {
     int issued, consumed;
 };
 
-// Copy the stage at c into the ring's next place (lane 0 issues).
-template <int PH>
-__device__ __forceinline__ void issue(const Params &p, const Shared *sm, Ring &r, Cur &c) {
-    if ((threadIdx.x & 31) == 0) {
-        const uint32_t s = static_cast<uint32_t>(r.issued & 1), st = r.base + s * kStageBytes, bar = r.bars + 8u * s;
-        const uint64_t pol = policy_evict_first();
-        const Mat &m = mat<PH>(p);
-        mbar_expect_tx_s(bar, kStageBytes);
-        tma3d(st, &m.tm_raw, 0, c.j, static_cast<int>(c.row16) * kRowsPerGroup, bar, pol);
-        tma3d(st + kRawStage, &m.tm_code, 0, c.j, static_cast<int>(c.row16) * kRowsPerGroup, bar, pol);
-    }
-    ++r.issued;
-    advance<PH>(p, sm, c);
-}
-
 // The end of a CTA: copies that a wait left in flight land, and the last CTA
-// leaves the workspace's words at zero.
+// sets the workspace's words back to zero.
 __device__ __forceinline__ void finish(const Params &p, Shared *sm, const Ring &rg) {
     if ((threadIdx.x & 31) == 0)
         for (int k = rg.consumed; k < rg.issued; ++k)
@@ -474,9 +425,6 @@ __device__ __forceinline__ void finish(const Params &p, Shared *sm, const Ring &
     __syncthreads();
     if (sm->last) {
         __threadfence();
-        if (ld_acquire(p.sync + kAbort))
-            for (uint32_t i = threadIdx.x; i < p.n_cnt; i += kThreads) p.cnt[i] = 0u;
-        __syncthreads();
         if (threadIdx.x < kSyncWords) p.sync[threadIdx.x] = 0u;
     }
 }
@@ -522,211 +470,11 @@ __device__ __forceinline__ void patch(uint32_t (&w)[8], uint2 C, uint32_t idx, u
 // ---------------------------------------------------------------------------
 // Results.
 
-// h of row group (seg, grp): lane (g, q) holds gate row f and up row f
-// (f = 8 grp + g) of pairs 2q, 2q+1 of each eight.
-template <int NT>
-__device__ __forceinline__ void store_hidden(const Params &p, const Shared *sm, const float (&a)[NT][4], uint32_t seg,
-                                             uint32_t grp) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int n = sm->seg_n[seg], first = sm->seg_first[seg], slots = p.tokens * p.top_k;
-    // the eight f of a row group are one piece; this lane's place in it
-    const int c8 = static_cast<int>(grp), in = c8 & 15;
-    const size_t base = piece_at(c8 >> 4, (in >> 1) & 3, in & 1, slots, first, in >> 3) +
-                        2 * (g < 4 ? 2 * g : 2 * (g - 4) + 1);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int b = nt * 8 + 2 * q + i;
-            if (b < n) {
-                const float gt = a[nt][i], hv = gt / (1.f + expf(-gt)) * a[nt][2 + i];
-                const __nv_bfloat16 hi = __float2bfloat16_rn(hv);
-                const float rest = hv - __bfloat162float(hi);
-                // (an infinite h has no rest)
-                const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(rest) < 3.4e38f ? rest : 0.f);
-                const size_t o = base + static_cast<size_t>(b) * 32;
-                *reinterpret_cast<uint16_t *>(p.hi + o) = __bfloat16_as_ushort(hi);
-                *reinterpret_cast<uint16_t *>(p.lo + o) = __bfloat16_as_ushort(lo);
-            }
-        }
-}
-
 __device__ __forceinline__ void put_y(const Params &p, size_t o, float v) {
     if (p.y_f32)
         static_cast<float *>(p.y)[o] = v;
     else
         static_cast<uint16_t *>(p.y)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
-// d of row group (seg, grp); the last segment of the row group adds up y.
-template <int NT>
-__device__ __forceinline__ void store_down(const Params &p, const Shared *sm, const float (&a)[NT][4], uint32_t seg,
-                                           uint32_t grp) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int n = sm->seg_n[seg], first = sm->seg_first[seg];
-    const size_t r = static_cast<size_t>(grp) * kRowsPerGroup + g;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int b = nt * 8 + 2 * q + (i & 1);
-            if (b < n) __stcg(p.d + static_cast<size_t>(sm->list[first + b]) * p.H + r + (i >= 2 ? 8 : 0), a[nt][i]);
-        }
-    __threadfence();
-    __syncwarp();
-    uint32_t prev = 0;
-    if (lane == 0) prev = atomicAdd(p.cnt + p.cnt_y + grp, 1u);
-    prev = __shfl_sync(0xFFFFFFFFu, prev, 0);
-    if (prev + 1 != static_cast<uint32_t>(sm->n_segs)) return;
-    __threadfence();
-    if (lane == 0) atomicExch(p.cnt + p.cnt_y + grp, 0u);
-    const size_t col = static_cast<size_t>(grp) * kRowsPerGroup + (lane & 15);
-    for (int t = lane >> 4; t < p.tokens; t += 2) {
-        float y = 0.f;
-        for (int s = 0; s < p.top_k; ++s) {
-            const int i = t * p.top_k + s;
-            if (sm->expert[i] >= 0) y = fmaf(sm->weight[i], __ldcg(p.d + static_cast<size_t>(i) * p.H + col), y);
-        }
-        put_y(p, static_cast<size_t>(t) * p.H + col, y);
-    }
-}
-
-template <int NT, int PH>
-__device__ __noinline__ void store_group(const Params &p, const Shared *sm, const float (&a)[NT][4], uint32_t gi) {
-    uint32_t seg, grp;
-    split<PH>(p, sm, gi, seg, grp);
-    if (PH == 1)
-        store_hidden<NT>(p, sm, a, seg, grp);
-    else
-        store_down<NT>(p, sm, a, seg, grp);
-}
-
-// ---------------------------------------------------------------------------
-// Row groups shared by warps.  Slot 0 of a warp (or CTA): the group that its
-// range starts in; slot 1: the one that it ends in.
-
-template <int NT>
-__device__ __forceinline__ float4 *warp_slot(const Params &p, float4 *parts, int warp, int slot) {
-    if (NT == 1) return parts + (warp * 2 + slot) * 32;
-    return reinterpret_cast<float4 *>(p.warp_part) +
-           ((static_cast<size_t>(blockIdx.x) * kWarps + warp) * 2 + slot) * NT * 32;
-}
-
-template <int NT>
-__device__ __forceinline__ float4 *cta_slot(const Params &p, size_t cta, int slot) {
-    return reinterpret_cast<float4 *>(p.cta_part) + (cta * 2 + slot) * NT * 32;
-}
-
-// The deal of a step's stages.
-struct Deal {
-    long long n_stages;
-    int n_units;
-    uint32_t S;
-    uint32_t cnt0;  // the step's first arrival counter
-
-    __device__ __forceinline__ long long start(long long unit) const { return unit_start(unit, n_stages, n_units); }
-};
-
-// Parts of a group that crosses CTAs: this CTA's goes to its slot, the last
-// CTA to arrive adds all in CTA order.
-template <int NT, int PH>
-__device__ __noinline__ void join_ctas(const Params &p, const Shared *sm, const Deal &dl, float (&a)[NT][4],
-                                       uint32_t gi) {
-    const int lane = threadIdx.x & 31, n_ctas = gridDim.x;
-    const long long c = blockIdx.x, c0 = dl.start(c * kWarps);
-    const long long g0 = static_cast<long long>(gi) * dl.S, g1 = g0 + dl.S;
-    float4 *mine = cta_slot<NT>(p, c, g0 <= c0 ? 0 : 1);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        __stcg(mine + nt * 32 + lane, make_float4(a[nt][0], a[nt][1], a[nt][2], a[nt][3]));
-    __threadfence();
-    __syncwarp();
-    long long cf = c, cl = c;
-    while (cf > 0 && dl.start(cf * kWarps) > g0) --cf;
-    while (cl + 1 < n_ctas && dl.start((cl + 1) * kWarps) < g1) ++cl;
-    // (CTAs without a stage of their own hand in nothing)
-    uint32_t want = 0;
-    for (long long v = cf; v <= cl; ++v) want += dl.start(v * kWarps) < dl.start((v + 1) * kWarps) ? 1u : 0u;
-    uint32_t prev = 0;
-    if (lane == 0) prev = atomicAdd(p.cnt + dl.cnt0 + gi, 1u);
-    prev = __shfl_sync(0xFFFFFFFFu, prev, 0);
-    if (prev + 1 != want) return;
-    __threadfence();
-    if (lane == 0) atomicExch(p.cnt + dl.cnt0 + gi, 0u);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[nt][i] = 0.f;
-    for (long long v = cf; v <= cl; ++v) {
-        const long long vs = dl.start(v * kWarps);
-        if (vs >= dl.start((v + 1) * kWarps)) continue;
-        const float4 *src = cta_slot<NT>(p, v, g0 <= vs ? 0 : 1);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const float4 t = __ldcg(src + nt * 32 + lane);
-            a[nt][0] += t.x;
-            a[nt][1] += t.y;
-            a[nt][2] += t.z;
-            a[nt][3] += t.w;
-        }
-    }
-    store_group<NT, PH>(p, sm, a, gi);
-}
-
-// After every warp's parts are in place: each shared group is completed by
-// the warp that holds its first stage in this CTA.
-template <int NT, int PH>
-__device__ __noinline__ void join_warps(const Params &p, const Shared *sm, float4 *parts, const Deal &dl) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long u = static_cast<long long>(blockIdx.x) * kWarps;
-    const long long bnd = dl.start(u + (lane <= kWarps ? lane : kWarps));
-    auto boundary = [&](int i) { return static_cast<long long>(__shfl_sync(0xFFFFFFFFu, bnd, i)); };
-    const long long c0 = boundary(0), c1 = boundary(kWarps);
-    const long long wb = boundary(warp), we = boundary(warp + 1);
-    if (wb >= we) return;
-    const uint32_t first = static_cast<uint32_t>(wb) / dl.S, last = static_cast<uint32_t>(we - 1) / dl.S;
-    for (int k = 0; k < 2; ++k) {
-        const uint32_t gi = k ? last : first;
-        if (k && last == first) break;
-        const long long g0 = static_cast<long long>(gi) * dl.S, g1 = g0 + dl.S;
-        if (g0 >= wb && g1 <= we) continue;        // whole in this warp: stored already
-        if ((g0 > c0 ? g0 : c0) < wb) continue;    // an earlier warp completes it
-        float a[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[nt][i] = 0.f;
-        for (int v = warp; v < kWarps; ++v) {
-            const long long vb = boundary(v), ve = boundary(v + 1);
-            if (vb >= g1) break;
-            if (vb >= ve) continue;
-            const float4 *src = warp_slot<NT>(p, parts, v, g0 <= vb ? 0 : 1);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float4 t = src[nt * 32 + lane];
-                a[nt][0] += t.x;
-                a[nt][1] += t.y;
-                a[nt][2] += t.z;
-                a[nt][3] += t.w;
-            }
-        }
-        if (g0 >= c0 && g1 <= c1)
-            store_group<NT, PH>(p, sm, a, gi);
-        else
-            join_ctas<NT, PH>(p, sm, dl, a, gi);
-    }
-}
-
-// ---------------------------------------------------------------------------
-// One step's products by one warp.
-
-template <int V, class M>
-__device__ __forceinline__ Meta load_meta(const M &m, const Cur &c, int len, int g, int tq, bool row_start) {
-    const int r = static_cast<int>(c.row16) * kRowsPerGroup + g;
-    Meta o;
-    load_row_meta<V>(m, r, c.j, len, tq, row_start, o.a0, o.a1, o.a2);
-    load_row_meta<V>(m, r + 8, c.j, len, tq, row_start, o.b0, o.b1, o.b2);
-    return o;
 }
 
 // The lane's 16 values of one half chunk pair (two pieces).
@@ -745,258 +493,6 @@ __device__ __forceinline__ void chunk_mma(float (&acc)[4], const uint32_t (&wa)[
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         mma16816(acc, wa[2 * i], wb[2 * i], wa[2 * i + 1], wb[2 * i + 1], xw[2 * i], xw[2 * i + 1]);
-}
-
-// The warp's range of step PH; `pc` is the next stage to copy (the first
-// ones are in flight).  False when a wait gave up.
-template <int V, int NT, int PH>
-__device__ __forceinline__ bool products(const Params &p, const Shared *sm, float4 *parts, Ring &rg, Cur pc,
-                                         const Deal &dl, long long s0, int n) {
-    constexpr int kChains = NT == 1 ? 2 : 1;  // independent sums, so that products do not wait for one another
-    const Mat &m = mat<PH>(p);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, q = lane & 3, tq = q >> 1, qh = q & 1;
-    const int nx = PH == 1 ? p.tokens : p.tokens * p.top_k;  // rows of x or h
-    const size_t half = static_cast<size_t>(nx) * 32, chunk_bytes = 2 * half;
-    // the lane's places in a stage ([row][tile][bytes], swizzled by the copies)
-    const uint32_t line = static_cast<uint32_t>(2 * g + tq), rsw = line & 7u, csw = static_cast<uint32_t>(g) & 3u;
-    const uint32_t oR = line * 128u, oC = kRawStage + line * 64u;
-
-    Cur cc = locate<PH>(p, sm, static_cast<uint32_t>(s0), n), cn = cc;
-    int len = min(kNT, m.T - cc.j);
-    Meta mc = load_meta<V>(m, cc, len, g, tq, true);
-    uint32_t runA = 0, runB = 0;
-    if (V == 2) {
-        const int r = static_cast<int>(cc.row16) * kRowsPerGroup + g;
-        runA = mc.a2 + prefix_count_v2(m, r, cc.j, q);
-        runB = mc.b2 + prefix_count_v2(m, r + 8, cc.j, q);
-    }
-    advance<PH>(p, sm, cn);
-
-    float acc[kChains][NT][4];
-    uint32_t xoff[NT];
-    int nts = 0;  // eights of pairs in the current segment
-    bool fresh = true;
-    while (cc.left > 0) {
-        if (fresh) {
-            fresh = false;
-            uint32_t seg, grp;
-            split<PH>(p, sm, cc.gi, seg, grp);
-            const int pairs = sm->seg_n[seg], first = sm->seg_first[seg];
-            nts = (pairs + 7) >> 3;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                // (columns past the last pair repeat it; their results are dropped)
-                const int at = first + min(nt * 8 + g, pairs - 1);
-                xoff[nt] = static_cast<uint32_t>((PH == 1 ? sm->list[at] / p.top_k : at) * 32 + qh * 16);
-#pragma unroll
-                for (int k = 0; k < kChains; ++k)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[k][nt][i] = 0.f;
-            }
-        }
-        int lenn = 0;
-        Meta mn = {0u, 0u, 0u, 0u, 0u, 0u};
-        if (cn.left > 0) {
-            lenn = min(kNT, m.T - cn.j);
-            mn = load_meta<V>(m, cn, lenn, g, tq, cn.j == 0);
-        }
-        const uint32_t slot = static_cast<uint32_t>(rg.consumed & 1), bar = rg.bars + 8u * slot;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_s(bar, static_cast<uint32_t>(rg.consumed >> 1) & 1u))) {
-            if (lane == 0) give_up(p);
-            return false;
-        }
-        const uint32_t st = rg.base + slot * kStageBytes;
-        const bool live = tq < len;  // the lane's tile belongs to this stage (else zeros from the copy)
-        uint32_t bA, sA, eA, bB, sB, eB;
-        row_span<V>(mc.a0, mc.a1, mc.a2, tq, runA, bA, sA, eA);
-        row_span<V>(mc.b0, mc.b1, mc.b2, tq, runB, bB, sB, eB);
-        const uint4 cA0 = lds128(st + oC + (((2u * qh) ^ csw) << 4));
-        const uint4 cA1 = lds128(st + oC + (((2u * qh + 1u) ^ csw) << 4));
-        const uint4 cB0 = lds128(st + oC + (((2u * qh) ^ csw) << 4) + 1024);
-        const uint4 cB1 = lds128(st + oC + (((2u * qh + 1u) ^ csw) << 4) + 1024);
-        if (p.err && (bA > static_cast<uint32_t>(kMaxBase) || bB > static_cast<uint32_t>(kMaxBase)))
-            raise_flag(p.err, S12_FLAG_BASE);
-        const bool anyesc = __any_sync(0xFFFFFFFFu, eA != sA || eB != sB);
-        const uint32_t B2A = bA * 0x00800080u, B2B = bB * 0x00800080u;
-        const size_t at = static_cast<size_t>(cc.j + tq) * 4 * chunk_bytes;
-        const uint8_t *x0 = (PH == 1 ? p.xp : p.hi) + at, *x1 = p.lo + at;
-
-        auto multiply = [&](int c, const uint32_t (&wa)[8], const uint32_t (&wb)[8], float (&a)[NT][4]) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if (NT == 1 || nt < nts) {
-                    uint32_t xw[8];
-                    load_x(xw, x0 + xoff[nt] + c * chunk_bytes, half, live);
-                    chunk_mma(a[nt], wa, wb, xw);
-                    if (PH == 2) {
-                        load_x(xw, x1 + xoff[nt] + c * chunk_bytes, half, live);
-                        chunk_mma(a[nt], wa, wb, xw);
-                    }
-                }
-        };
-        auto refill = [&]() {
-            // the stage is in registers: hand it back to the copy engine
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (pc.left > 0) issue<PH>(p, sm, rg, pc);
-        };
-        if (!anyesc) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 rA = lds128(st + oR + (((4u * qh + c) ^ rsw) << 4));
-                const uint4 rB = lds128(st + oR + (((4u * qh + c) ^ rsw) << 4) + 2048);
-                if (c == 3) refill();
-                const uint4 kA = c < 2 ? cA0 : cA1, kB = c < 2 ? cB0 : cB1;
-                uint32_t wa[8], wb[8];
-                decode_pairs(rA.x, rA.y, c & 1 ? kA.z : kA.x, B2A, wa);
-                decode_pairs(rA.z, rA.w, c & 1 ? kA.w : kA.y, B2A, wa + 4);
-                decode_pairs(rB.x, rB.y, c & 1 ? kB.z : kB.x, B2B, wb);
-                decode_pairs(rB.z, rB.w, c & 1 ? kB.w : kB.y, B2B, wb + 4);
-                multiply(c, wa, wb, acc[c & (kChains - 1)]);
-            }
-        } else {
-            // some row of the stage has escapes: a compact loop (its first
-            // half of a tile row counts from the span's start, the second
-            // half back from its end)
-            const uint32_t nA = chunk_counts(cA0, cA1), nB = chunk_counts(cB0, cB1);
-            const uint32_t allA = (nA * 0x01010101u) >> 24, allB = (nB * 0x01010101u) >> 24;
-            const uint32_t pairA = allA + __shfl_xor_sync(0xFFFFFFFFu, allA, 1);
-            const uint32_t pairB = allB + __shfl_xor_sync(0xFFFFFFFFu, allB, 1);
-            if (p.err && live && qh == 0 && (pairA != eA - sA || pairB != eB - sB))
-                raise_flag(p.err, S12_FLAG_ESC_COUNT);
-            uint32_t iA = qh ? eA - allA : sA, iB = qh ? eB - allB : sB;
-            const uint32_t limA = sA <= eA ? min(eA, m.n_esc) : 0u, limB = sB <= eB ? min(eB, m.n_esc) : 0u;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                const uint4 rA = lds128(st + oR + (((4u * qh + c) ^ rsw) << 4));
-                const uint4 rB = lds128(st + oR + (((4u * qh + c) ^ rsw) << 4) + 2048);
-                const uint32_t piece = st + oC + (((2u * qh + (c >> 1)) ^ csw) << 4) + 8u * (c & 1);
-                const uint2 kA = lds64(piece), kB = lds64(piece + 1024);
-                uint32_t wa[8], wb[8];
-                decode_pairs(rA.x, rA.y, kA.x, B2A, wa);
-                decode_pairs(rA.z, rA.w, kA.y, B2A, wa + 4);
-                decode_pairs(rB.x, rB.y, kB.x, B2B, wb);
-                decode_pairs(rB.z, rB.w, kB.y, B2B, wb + 4);
-                const uint32_t hereA = (nA >> (8 * c)) & 0xFFu, hereB = (nB >> (8 * c)) & 0xFFu;
-                if (hereA) patch(wa, kA, iA, limA, m.esc, p.err);
-                if (hereB) patch(wb, kB, iB, limB, m.esc, p.err);
-                iA += hereA;
-                iB += hereB;
-                multiply(c, wa, wb, acc[0]);
-            }
-            refill();
-        }
-        ++rg.consumed;
-        if (cn.gi != cc.gi || cn.left == 0) {
-            // the range leaves this row group
-            if (kChains == 2)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[0][0][i] += acc[kChains - 1][0][i];
-            const long long g0 = static_cast<long long>(cc.gi) * dl.S;
-            if (g0 >= s0 && g0 + dl.S <= s0 + n) {
-                // (a copy: only it has an address, the sums stay in registers)
-                float a[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) a[nt][i] = acc[0][nt][i];
-                store_group<NT, PH>(p, sm, a, cc.gi);
-            } else {
-                float4 *dst = warp_slot<NT>(p, parts, warp, g0 <= s0 ? 0 : 1);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    dst[nt * 32 + lane] = make_float4(acc[0][nt][0], acc[0][nt][1], acc[0][nt][2], acc[0][nt][3]);
-            }
-            fresh = true;
-            if (V == 2) {
-                runA = mn.a2;
-                runB = mn.b2;
-            }
-        }
-        cc = cn;
-        len = lenn;
-        mc = mn;
-        if (cn.left > 0) advance<PH>(p, sm, cn);
-    }
-    return true;
-}
-
-template <int PH>
-__device__ __forceinline__ Deal deal(const Params &p, const Shared *sm) {
-    const Mat &m = mat<PH>(p);
-    Deal d;
-    d.S = m.S;
-    d.n_stages = static_cast<long long>(sm->n_segs) * m.G * m.S;
-    d.n_units = static_cast<int>(gridDim.x) * kWarps;
-    d.cnt0 = PH == 1 ? 0u : p.cnt_down;
-    return d;
-}
-
-// Both steps with NT eights of pairs a segment at most.
-template <int V, int NT>
-__device__ __noinline__ Ring layer(const Params &p, Shared *sm, float4 *parts, Ring rg) {
-    const long long u = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const Deal d1 = deal<1>(p, sm), d2 = deal<2>(p, sm);
-    const long long s1 = d1.start(u), s2 = d2.start(u);
-    const int n1 = static_cast<int>(d1.start(u + 1) - s1), n2 = static_cast<int>(d2.start(u + 1) - s2);
-    Cur pc = locate<1>(p, sm, static_cast<uint32_t>(s1), n1);
-    for (int k = 0; k < kStages && pc.left > 0; ++k) issue<1>(p, sm, rg, pc);
-    bool ok = n1 == 0 || products<V, NT, 1>(p, sm, parts, rg, pc, d1, s1, n1);
-    // the first copies of step 2 run while the grid meets
-    pc = locate<2>(p, sm, static_cast<uint32_t>(s2), n2);
-    if (ok)
-        for (int k = 0; k < kStages && pc.left > 0; ++k) issue<2>(p, sm, rg, pc);
-    __syncthreads();
-    join_warps<NT, 1>(p, sm, parts, d1);
-    if (!grid_meet(p, sm, kBarHidden)) return rg;
-    if (ok && n2 > 0) products<V, NT, 2>(p, sm, parts, rg, pc, d2, s2, n2);
-    __syncthreads();
-    join_warps<NT, 2>(p, sm, parts, d2);
-    return rg;
-}
-
-template <int V>
-__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ Params p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    float4 *parts = reinterpret_cast<float4 *>(base + kRingBytes);
-    Shared *sm = reinterpret_cast<Shared *>(base + kRingBytes + kWarps * 2 * kPartBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Ring rg;
-    rg.bars = smem_addr(sm->bars) + static_cast<uint32_t>(warp) * kStages * 8u;
-    rg.base = smem_addr(base) + static_cast<uint32_t>(warp) * kStages * kStageBytes;
-    rg.issued = rg.consumed = 0;
-    if (lane == 0) {
-        for (int s = 0; s < kStages; ++s) mbar_init_s(rg.bars + 8u * s, 1);
-        fence_barrier_init();
-    }
-    pack_x(p, p.xp, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
-    if (!p.ids_in) {
-        // many scores: 4 x 4 to a warp, so that x and the router are read a quarter as often
-        const int u0 = warp * gridDim.x + blockIdx.x, step = gridDim.x * kWarps;
-        if (p.tokens >= 8 && p.tokens * p.experts >= 1024)
-            score<4, 4>(p, p.scores, u0, step);
-        else
-            score<1, 1>(p, p.scores, u0, step);
-    }
-    if (grid_meet(p, sm, kBarRoute)) {
-        route(p, sm, p.scores);
-        if (sm->n_segs == 0) {
-            // no token goes anywhere
-            const size_t n = static_cast<size_t>(p.tokens) * p.H;
-            for (size_t i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) put_y(p, i, 0.f);
-        } else if (sm->most <= 8) {
-            rg = layer<V, 1>(p, sm, parts, rg);
-        } else if (sm->most <= 16) {
-            rg = layer<V, 2>(p, sm, parts, rg);
-        } else if (sm->most <= 32) {
-            rg = layer<V, 4>(p, sm, parts, rg);
-        } else {
-            rg = layer<V, 8>(p, sm, parts, rg);
-        }
-    }
-    finish(p, sm, rg);
 }
 
 // ---------------------------------------------------------------------------
@@ -1018,7 +514,7 @@ struct Step {
     uint32_t items;      // of the step: row groups by ranges
     uint32_t stages;     // of a range (the last range of a row group may have fewer)
     uint32_t ranges;     // of a row group
-    uint32_t m1, m2, d2;  // reciprocals of `ranges` and of d2, the row groups (step 1) or segments (step 2)
+    uint32_t m1, m2, d2;  // reciprocals of `ranges` and of d2, the blocks of row groups (step 1) or segments (step 2)
 };
 
 struct SmallShared {
@@ -1050,18 +546,19 @@ __device__ __forceinline__ Item item_at(const Step &st, uint32_t it) {
     return o;
 }
 
+// `per`: row groups that go together (of one segment).
 template <int PH>
-__device__ __forceinline__ void plan_step(const Params &p, SmallShared *sm) {
+__device__ __forceinline__ Step plan_step(const Params &p, const Shared *sm, int per) {
     const Mat &m = mat<PH>(p);
+    const uint32_t blocks = static_cast<uint32_t>((m.G + per - 1) / per), segs = static_cast<uint32_t>(sm->n_segs);
     Step st;
-    const uint32_t groups = static_cast<uint32_t>(sm->s.n_segs) * m.G;
-    st.stages = min(PH == 1 ? p.range_up : p.range_down, m.S);
+    st.stages = min(p.range, m.S);
     st.ranges = (m.S + st.stages - 1) / st.stages;
-    st.items = groups * st.ranges;
-    st.d2 = PH == 1 ? static_cast<uint32_t>(m.G) : static_cast<uint32_t>(sm->s.n_segs);
+    st.items = segs * blocks * st.ranges;
+    st.d2 = PH == 1 ? blocks : segs;
     st.m1 = reciprocal(st.ranges);
     st.m2 = reciprocal(st.d2);
-    sm->step[PH - 1] = st;
+    return st;
 }
 
 // One stage of a warp.
@@ -1245,8 +742,8 @@ __device__ __forceinline__ bool small_step(const Params &p, const SmallShared *s
     const Mat &m = mat<PH>(p);
     const Step &st = sm->step[PH - 1];
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, tq = q >> 1, qh = q & 1;
-    const int slots = p.tokens * p.top_k, nx = PH == 1 ? p.tokens : slots;  // rows of x or h
-    const uint32_t half = static_cast<uint32_t>(nx) * 32u, chunk_bytes = 2 * half;
+    const int slots = p.tokens * p.top_k;
+    uint32_t half = static_cast<uint32_t>(p.tokens) * 32u;  // (of step 2: the segment's pairs)
     const size_t rows = static_cast<size_t>(m.G) * kRowsPerGroup;  // of an expert
     float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains of products
     Words w0 = load_words<V>(m, d0);
@@ -1261,8 +758,13 @@ __device__ __forceinline__ bool small_step(const Params &p, const SmallShared *s
             const int first = sm->s.seg_first[at.seg];
             pairs = sm->s.seg_n[at.seg];
             // (columns past the last pair repeat it; their results are dropped)
-            const int i = first + min(g, pairs - 1);
-            xl = x + static_cast<size_t>(PH == 1 ? sm->s.token[i] : i) * 32 + qh * 16;
+            const int i = min(g, pairs - 1);
+            if (PH == 1) {
+                xl = x + static_cast<size_t>(sm->s.token[first + i]) * 32 + qh * 16;
+            } else {
+                half = static_cast<uint32_t>(pairs) * 32u;
+                xl = x + static_cast<size_t>(first) * p.F * 2 + i * 32 + qh * 16;
+            }
             to = (PH == 1 ? p.gu : p.d) + (static_cast<size_t>(at.range) * slots + first + 2 * q) * rows +
                  static_cast<size_t>(at.grp) * kRowsPerGroup + g;
         }
@@ -1272,6 +774,7 @@ __device__ __forceinline__ bool small_step(const Params &p, const SmallShared *s
             return false;
         }
         const bool live = d0.j + tq < m.T;  // the lane's tile exists (else zeros from the copy)
+        const uint32_t chunk_bytes = 2 * half;
         const size_t at = static_cast<size_t>(d0.j + tq) * 4 * chunk_bytes;
         const ptrdiff_t lo = PH == 2 ? p.lo - p.hi : 0;
         Desc d2;
@@ -1328,7 +831,7 @@ __device__ __forceinline__ float4 shfl4(const float4 &v, int from_xor) {
                        __shfl_xor_sync(0xFFFFFFFFu, v.z, from_xor), __shfl_xor_sync(0xFFFFFFFFu, v.w, from_xor));
 }
 
-// The 16 sums of a pair's row group over its ranges, 4 to a lane (lane & 3);
+// The sums of the 16 rows of a pair's row group over its ranges, 4 to a lane (lane & 3);
 // lanes 4 apart add every eighth range, then one another: a fixed order.
 __device__ __forceinline__ float4 sum_ranges(const float *src, size_t plane, uint32_t ranges) {
     const int lane = threadIdx.x & 31;
@@ -1345,13 +848,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Pairs of the list (the slots that are left out are not in it).
+__device__ __forceinline__ int used_pairs(const Shared *sm) {
+    const int last = sm->n_segs - 1;
+    return sm->seg_first[last] + sm->seg_n[last];
+}
+
 // h from the sums of step 1: a warp takes one pair's row group at a time.
-__device__ __forceinline__ void make_hidden(const Params &p, const SmallShared *sm) {
+__device__ __forceinline__ void make_hidden(const Params &p, const Shared *sm, uint32_t ranges) {
     const int lane = threadIdx.x & 31, slots = p.tokens * p.top_k;
-    const uint32_t G = static_cast<uint32_t>(p.up.G), ranges = sm->step[0].ranges;
-    const int last = sm->s.n_segs - 1, pairs = sm->s.seg_first[last] + sm->s.seg_n[last];  // that are in use
+    const uint32_t G = static_cast<uint32_t>(p.up.G), warps = blockDim.x >> 5;
+    const int pairs = used_pairs(sm);
     const size_t rows = static_cast<size_t>(G) * kRowsPerGroup, plane = static_cast<size_t>(slots) * rows;
-    for (uint32_t u = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < pairs * G; u += gridDim.x * kWarps) {
+    for (uint32_t u = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < pairs * G; u += gridDim.x * warps) {
         const uint32_t pos = u / G, grp = u - pos * G;
         const float4 v = sum_ranges(p.gu + pos * rows + static_cast<size_t>(grp) * kRowsPerGroup, plane, ranges);
         // lanes 0 and 1: gate rows 0-3 and 4-7; lanes 2 and 3: the up rows
@@ -1372,8 +881,10 @@ __device__ __forceinline__ void make_hidden(const Params &p, const SmallShared *
                 lo[i] = pack_bf16(fabsf(r0) < 3.4e38f ? r0 : 0.f, fabsf(r1) < 3.4e38f ? r1 : 0.f);
             }
             const int in = static_cast<int>(grp & 15u);
-            const size_t o = piece_at(static_cast<int>(grp >> 4), (in >> 1) & 3, in & 1, slots, static_cast<int>(pos),
-                                      in >> 3);
+            const int seg = sm->segment[pos], first = sm->seg_first[seg];
+            const size_t o = static_cast<size_t>(first) * p.F * 2 +
+                             piece_at(static_cast<int>(grp >> 4), (in >> 1) & 3, in & 1, sm->seg_n[seg],
+                                      static_cast<int>(pos) - first, in >> 3);
             *reinterpret_cast<uint4 *>(p.hi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(p.lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
@@ -1381,19 +892,19 @@ __device__ __forceinline__ void make_hidden(const Params &p, const SmallShared *
 }
 
 // y from the sums of step 2: a warp takes 16 values of a token at a time.
-__device__ __forceinline__ void make_y(const Params &p, const SmallShared *sm) {
+__device__ __forceinline__ void make_y(const Params &p, const Shared *sm, uint32_t ranges) {
     const int lane = threadIdx.x & 31, slots = p.tokens * p.top_k;
-    const uint32_t G = static_cast<uint32_t>(p.down.G), ranges = sm->step[1].ranges;
+    const uint32_t G = static_cast<uint32_t>(p.down.G), warps = blockDim.x >> 5;
     const size_t rows = static_cast<size_t>(G) * kRowsPerGroup, plane = static_cast<size_t>(slots) * rows;
-    for (uint32_t u = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < p.tokens * G; u += gridDim.x * kWarps) {
+    for (uint32_t u = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < p.tokens * G; u += gridDim.x * warps) {
         const uint32_t t = u / G, grp = u - t * G;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < p.top_k; ++s) {
             const int i = static_cast<int>(t) * p.top_k + s;
-            if (sm->s.expert[i] < 0) continue;
-            const float4 v = sum_ranges(p.d + sm->s.place[i] * rows + static_cast<size_t>(grp) * kRowsPerGroup, plane,
+            if (sm->expert[i] < 0) continue;
+            const float4 v = sum_ranges(p.d + sm->place[i] * rows + static_cast<size_t>(grp) * kRowsPerGroup, plane,
                                         ranges);
-            const float w = sm->s.weight[i];
+            const float w = sm->weight[i];
             y = make_float4(fmaf(w, v.x, y.x), fmaf(w, v.y, y.y), fmaf(w, v.z, y.z), fmaf(w, v.w, y.w));
         }
         if (lane < 4) {
@@ -1451,8 +962,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_small_kernel(const __grid_con
             const size_t n = static_cast<size_t>(p.tokens) * p.H;
             for (size_t i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) put_y(p, i, 0.f);
         } else {
-            if (threadIdx.x == 0) plan_step<1>(p, sm);
-            if (threadIdx.x == 32) plan_step<2>(p, sm);
+            if (threadIdx.x == 0) sm->step[0] = plan_step<1>(p, &sm->s, 1);
+            if (threadIdx.x == 32) sm->step[1] = plan_step<2>(p, &sm->s, 1);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scores give way to copies
             __syncthreads();
             Feed<1> f1;
@@ -1472,10 +983,381 @@ __global__ void __launch_bounds__(kThreads, 1) moe_small_kernel(const __grid_con
                 if (d1.live) issue_at<2>(p, rg, d1);
             }
             if (grid_meet(p, &sm->s, kBarSums)) {
-                make_hidden(p, sm);
+                make_hidden(p, &sm->s, sm->step[0].ranges);
                 if (grid_meet(p, &sm->s, kBarHidden)) {
                     if (ok) small_step<V, 2>(p, sm, p.hi, rg, f2, d0, d1);
-                    if (grid_meet(p, &sm->s, kBarDown)) make_y(p, sm);
+                    if (grid_meet(p, &sm->s, kBarDown)) make_y(p, &sm->s, sm->step[1].ranges);
+                }
+            }
+        }
+    }
+    finish(p, &sm->s, rg);
+}
+
+// ---------------------------------------------------------------------------
+// Many pairs an expert: up to 64 share a read of its weights.
+//
+// A unit is twelve row groups of a segment, one to a warp, by a range of
+// columns.  All warps of a CTA go through the same columns, so x is read from
+// shared memory, where a thirteenth warp copies it tile by tile (128 columns of
+// the segment's pairs) into a ring; through L1, with every warp at columns of
+// its own, x cost three times the weights' traffic to L2.  Units come from a
+// counter of the grid as items do above, claimed by the warp that copies x.
+
+constexpr int kMaxX = 16;   // places of the x ring
+constexpr int kUnits = 32;  // the queue: copying x is at most kMaxX units ahead of a warp
+
+struct LargeShared {
+    Shared s;
+    Step step[2];
+    unsigned long long queue[2][kUnits];         // ordinal << 32 | unit
+    unsigned long long full[2][kMaxX], empty[2][kMaxX];  // mbarriers of the x ring, by step
+    uint32_t abort;
+};
+
+struct Unit {
+    uint32_t seg, range, block;
+    int j, n;  // first tile; stages (0: no more units)
+};
+
+// The CTA's unit `ord` (the queue's answer may have to be waited for, with a limit).
+template <int PH>
+__device__ __forceinline__ Unit unit_at(const Params &p, LargeShared *sm, uint32_t ord) {
+    const Step &st = sm->step[PH - 1];
+    Unit o = {0u, 0u, 0u, 0, 0};
+    const volatile unsigned long long *at = &sm->queue[PH - 1][ord % kUnits];
+    unsigned long long e = *at;
+    if (e >> 32 != ord) {
+        const long long t0 = clock64();
+        while (e >> 32 != ord) {
+            if (*const_cast<volatile uint32_t *>(&sm->abort)) return o;
+            if (clock64() - t0 > kWaitCycles) {
+                sm->abort = 1u;
+                give_up(p);
+                return o;
+            }
+            e = *at;
+        }
+    }
+    const uint32_t it = static_cast<uint32_t>(e);
+    if (it >= st.items) return o;
+    const Item i = item_at<PH>(st, it);
+    o.seg = i.seg;
+    o.range = i.range;
+    o.block = i.grp;
+    o.j = static_cast<int>(i.range * st.stages) * kNT;
+    o.n = static_cast<int>(min(st.stages, mat<PH>(p).S - i.range * st.stages));
+    return o;
+}
+
+// The x ring in a step: places of `bytes` bytes, n of them (even, so that the
+// two tiles of a stage lie 64 bytes apart modulo 128 and their reads share no
+// bank).
+struct XRing {
+    uint32_t base, bytes, n;
+    uint32_t at, parity;  // the next place and its phase
+
+    __device__ __forceinline__ void advance() {
+        if (++at == n) {
+            at = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+template <int PH>
+__device__ __forceinline__ XRing x_ring(const Params &p, const LargeShared *sm, uint32_t base) {
+    XRing x;
+    x.base = base;
+    x.bytes = static_cast<uint32_t>(sm->s.most) * 256u * PH + 64u;  // (h: two planes)
+    x.n = min(static_cast<uint32_t>(kMaxX), p.pool / x.bytes) & ~1u;
+    x.at = x.parity = 0;
+    return x;
+}
+
+// A step by the thread that copies x.
+template <int PH>
+__device__ __forceinline__ void copy_x(const Params &p, LargeShared *sm, uint32_t base) {
+    XRing xr = x_ring<PH>(p, sm, base);
+    const int T = mat<PH>(p).T;
+    const size_t row = static_cast<size_t>(T) * kTile * 2;  // bytes of a pair's row
+    uint32_t issued = 0;
+    bool ok = true;
+    for (uint32_t ord = 0; ok; ++ord) {
+        const Unit u = unit_at<PH>(p, sm, ord);
+        if (u.n == 0) break;
+        const uint32_t claimed = atomicAdd(p.sync + (PH == 1 ? kNext1 : kNext2), 1u) + kAhead * gridDim.x;
+        const uint32_t bytes = static_cast<uint32_t>(sm->s.seg_n[u.seg]) * 256u;
+        const size_t off = sm->s.seg_first[u.seg] * row;
+        for (int t = u.j; ok && t < min(u.j + kNT * u.n, T); ++t) {
+            const uint32_t full = smem_addr(&sm->full[PH - 1][xr.at]), dst = xr.base + xr.at * xr.bytes;
+            ok = mbar_wait_s(smem_addr(&sm->empty[PH - 1][xr.at]), xr.parity ^ 1u);
+            if (!ok) break;
+            mbar_expect_tx_s(full, PH * bytes);
+            const size_t src = off + static_cast<size_t>(t) * bytes;
+#pragma unroll
+            for (int plane = 0; plane < PH; ++plane)
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                        dst + plane * bytes),
+                    "l"((PH == 1 ? p.xp : plane ? p.lo : p.hi) + src), "r"(bytes), "r"(full)
+                    : "memory");
+            xr.advance();
+            ++issued;
+        }
+        const uint32_t next = ord + kAhead;
+        *const_cast<volatile unsigned long long *>(&sm->queue[PH - 1][next % kUnits]) =
+            (static_cast<unsigned long long>(next) << 32) | claimed;
+    }
+    if (!ok) {
+        sm->abort = 1u;
+        give_up(p);
+    }
+    // every copy lands before the CTA goes on
+    for (uint32_t i = issued > xr.n ? issued - xr.n : 0; i < issued; ++i)
+        mbar_wait_s(smem_addr(&sm->full[PH - 1][i % xr.n]), (i / xr.n) & 1u);
+}
+
+__device__ __forceinline__ void arrive_s(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A warp's way through the weights of a step: its next stage, unit after unit.
+// A unit that has no row group for the warp has stages that are not live: a
+// warp that looked past them for its next row group would wait for units that
+// are claimed only when it has let go of the x of this one.
+template <int PH>
+struct LargeFeed {
+    Unit u;
+    uint32_t ord;
+    int k;
+
+    __device__ __forceinline__ void start(const Params &p, LargeShared *sm) {
+        ord = 0;
+        k = 0;
+        u = unit_at<PH>(p, sm, 0);
+    }
+
+    __device__ __forceinline__ Desc next(const Params &p, LargeShared *sm) {
+        const Mat &m = mat<PH>(p);
+        Desc d;
+        d.live = d.last = false;
+        d.it = d.row16 = 0;
+        d.j = 0;
+        if (u.n && k == u.n) {
+            k = 0;
+            u = unit_at<PH>(p, sm, ++ord);
+        }
+        if (u.n) {
+            const uint32_t grp = u.block * kLargeWarps + (threadIdx.x >> 5);
+            d.row16 = sm->s.seg_expert[u.seg] * static_cast<uint32_t>(m.G) + grp;
+            d.j = u.j + kNT * k;
+            d.live = grp < static_cast<uint32_t>(m.G);
+            ++k;
+        }
+        return d;
+    }
+};
+
+// A step by one of the warps that multiply.  d0 and d1 are its first stages,
+// whose copies are in flight.  False when a wait gave up.
+template <int V, int PH, int NT>
+__device__ __forceinline__ bool large_step(const Params &p, LargeShared *sm, uint32_t xbase, Ring &rg,
+                                           LargeFeed<PH> &feed, Desc d0, Desc d1) {
+    const Mat &m = mat<PH>(p);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, tq = q >> 1, qh = q & 1;
+    const int slots = p.tokens * p.top_k;
+    const size_t rows = static_cast<size_t>(m.G) * kRowsPerGroup;  // of an expert
+    XRing xr = x_ring<PH>(p, sm, xbase);
+    Words w0 = load_words<V>(m, d0);
+    for (uint32_t ord = 0;; ++ord) {
+        const Unit u = unit_at<PH>(p, sm, ord);
+        if (u.n == 0) break;
+        const uint32_t grp = u.block * kLargeWarps + warp;
+        const bool mine = grp < static_cast<uint32_t>(m.G);  // (the last unit of a segment may have fewer groups)
+        const int pairs = sm->s.seg_n[u.seg], first = sm->s.seg_first[u.seg], nts = (pairs + 7) >> 3;
+        const uint32_t half = static_cast<uint32_t>(pairs) * 32u;
+        // (columns past the last pair repeat it; their results are dropped)
+        const uint32_t off = static_cast<uint32_t>(g) * 32u + qh * 16u;
+        const uint32_t off_last = static_cast<uint32_t>(min(8 * (nts - 1) + g, pairs - 1)) * 32u + qh * 16u;
+        float acc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < u.n; ++k) {
+            const bool two = u.j + kNT * k + 1 < m.T;
+            XRing x1 = xr;
+            x1.advance();
+            const uint32_t slot = static_cast<uint32_t>(rg.consumed & 1);
+            bool ok = mbar_wait_s(smem_addr(&sm->full[PH - 1][xr.at]), xr.parity);
+            if (ok && two) ok = mbar_wait_s(smem_addr(&sm->full[PH - 1][x1.at]), x1.parity);
+            if (ok && mine) ok = mbar_wait_s(rg.bars + 8u * slot, static_cast<uint32_t>(rg.consumed >> 1) & 1u);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                if (lane == 0) give_up(p);
+                sm->abort = 1u;
+                return false;
+            }
+            const Words w1 = load_words<V>(m, d1);
+            Desc d2;
+            if (mine) {
+                const bool live = two || tq == 0;  // the lane's tile exists (else zeros from the copy)
+                const uint32_t xl = xr.base + (tq ? x1.at : xr.at) * xr.bytes;
+                auto multiply = [&](int c, const uint32_t (&wa)[8], const uint32_t (&wb)[8]) {
+                    const uint32_t xc = xl + 2u * c * half;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        if (nt < nts) {
+                            const uint32_t at = xc + (nt + 1 == nts ? off_last : off + 256u * nt);
+#pragma unroll
+                            for (int plane = 0; plane < PH; ++plane) {
+                                uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+                                if (live) {
+                                    a = lds128(at + plane * 8u * half);
+                                    b = lds128(at + plane * 8u * half + half);
+                                }
+                                const uint32_t xw[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                                chunk_mma(acc[nt], wa, wb, xw);
+                            }
+                        }
+                };
+                auto refill = [&]() {
+                    // the stage is in registers: hand it back to the copy
+                    // engine.  (It was read only, which needs no proxy fence.)
+                    __syncwarp();
+                    d2 = feed.next(p, sm);
+                    if (d2.live) issue_at<PH>(p, rg, d2);
+                };
+                stage_products<V>(p, m, d0, w0, rg.base + slot * kStageBytes, multiply, refill);
+                ++rg.consumed;
+            } else {
+                d2 = feed.next(p, sm);
+                if (d2.live) issue_at<PH>(p, rg, d2);
+            }
+            d0 = d1;
+            d1 = d2;
+            w0 = w1;
+            __syncwarp();
+            if (lane == 0) {
+                arrive_s(smem_addr(&sm->empty[PH - 1][xr.at]));
+                if (two) arrive_s(smem_addr(&sm->empty[PH - 1][x1.at]));
+            }
+            xr.advance();
+            if (two) xr.advance();
+        }
+        if (!mine) continue;
+        // lane (g, q) holds rows g and g + 8 of pairs 2q and 2q + 1 of each eight
+        float *to = (PH == 1 ? p.gu : p.d) + (static_cast<size_t>(u.range) * slots + first + 2 * q) * rows +
+                    static_cast<size_t>(grp) * kRowsPerGroup + g;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (8 * nt + 2 * q + e < pairs) {
+                    __stcg(to + (8 * nt + e) * rows, acc[nt][e]);
+                    __stcg(to + (8 * nt + e) * rows + 8, acc[nt][2 + e]);
+                }
+    }
+    return true;
+}
+
+template <int V, int PH>
+__device__ __forceinline__ bool large_step(const Params &p, LargeShared *sm, uint32_t xbase, Ring &rg,
+                                           LargeFeed<PH> &feed, const Desc &d0, const Desc &d1) {
+    if (sm->s.most <= 16) return large_step<V, PH, 2>(p, sm, xbase, rg, feed, d0, d1);
+    if (sm->s.most <= 32) return large_step<V, PH, 4>(p, sm, xbase, rg, feed, d0, d1);
+    return large_step<V, PH, 8>(p, sm, xbase, rg, feed, d0, d1);
+}
+
+// The x that this thread wrote goes to copies (by other SMs, after the grid met).
+__device__ __forceinline__ void fence_for_copies() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+template <int V>
+__global__ void __launch_bounds__(kLargeThreads, 1) moe_large_kernel(const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    LargeShared *sm = reinterpret_cast<LargeShared *>(base + kLargeRingBytes);
+    const uint32_t xbase = smem_addr(base) + kLargeRingBytes + ((sizeof(LargeShared) + 127) & ~size_t(127));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool copies_x = warp == kLargeWarps;
+    Ring rg;
+    rg.bars = smem_addr(sm->s.bars) + static_cast<uint32_t>(warp) * kStages * 8u;
+    rg.base = smem_addr(base) + static_cast<uint32_t>(warp) * kStages * kStageBytes;
+    rg.issued = rg.consumed = 0;
+    if (lane == 0) {
+        if (copies_x) {
+            for (int i = 0; i < 2 * kMaxX; ++i) {
+                mbar_init_s(smem_addr(&sm->full[0][0] + i), 1);
+                mbar_init_s(smem_addr(&sm->empty[0][0] + i), kLargeWarps);
+            }
+        } else {
+            for (int s = 0; s < kStages; ++s) mbar_init_s(rg.bars + 8u * s, 1);
+        }
+        fence_barrier_init();
+    }
+    bool ok = true;
+    if (!p.ids_in) {
+        const int warps = kLargeWarps + 1, u0 = warp * gridDim.x + blockIdx.x, step = gridDim.x * warps;
+        if (p.tokens * p.experts >= 1024)
+            score<4, 4>(p, p.scores, u0, step);
+        else
+            score<1, 1>(p, p.scores, u0, step);
+        ok = grid_meet(p, &sm->s, kBarRoute);
+    }
+    if (ok) {
+        route(p, &sm->s, p.scores);
+        if (sm->s.n_segs == 0) {
+            // no token goes anywhere
+            const size_t n = static_cast<size_t>(p.tokens) * p.H;
+            for (size_t i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) put_y(p, i, 0.f);
+        } else {
+            if (threadIdx.x == 0) sm->step[0] = plan_step<1>(p, &sm->s, kLargeWarps);
+            if (threadIdx.x == 32) sm->step[1] = plan_step<2>(p, &sm->s, kLargeWarps);
+            if (threadIdx.x >= 64 && threadIdx.x < 64 + 2 * kUnits) {
+                const uint32_t k = threadIdx.x % kUnits;
+                sm->queue[(threadIdx.x - 64) / kUnits][k] =
+                    k < kAhead ? (static_cast<unsigned long long>(k) << 32) | (blockIdx.x + k * gridDim.x) : ~0ull;
+            }
+            if (threadIdx.x == 128) sm->abort = 0u;
+            pack_sorted(p, &sm->s, used_pairs(&sm->s));
+            fence_for_copies();
+            __syncthreads();
+            LargeFeed<1> f1;
+            LargeFeed<2> f2;
+            Desc d0, d1;
+            auto begin = [&](auto &f, auto ph) {
+                constexpr int PH = decltype(ph)::value;
+                f.start(p, sm);
+                d0 = f.next(p, sm);
+                if (d0.live) issue_at<PH>(p, rg, d0);
+                d1 = f.next(p, sm);
+                if (d1.live) issue_at<PH>(p, rg, d1);
+            };
+            // the first weights are copied while the grid meets
+            if (!copies_x) begin(f1, std::integral_constant<int, 1>());
+            if (grid_meet(p, &sm->s, kBarPack)) {
+                fence_for_copies();
+                if (copies_x) {
+                    if (lane == 0) copy_x<1>(p, sm, xbase);
+                    __syncwarp();
+                } else {
+                    ok = large_step<V, 1>(p, sm, xbase, rg, f1, d0, d1);
+                    if (ok) begin(f2, std::integral_constant<int, 2>());
+                }
+                if (grid_meet(p, &sm->s, kBarSums)) {
+                    make_hidden(p, &sm->s, sm->step[0].ranges);
+                    fence_for_copies();
+                    if (grid_meet(p, &sm->s, kBarHidden)) {
+                        fence_for_copies();
+                        if (copies_x) {
+                            if (lane == 0) copy_x<2>(p, sm, xbase);
+                            __syncwarp();
+                        } else if (ok) {
+                            large_step<V, 2>(p, sm, xbase, rg, f2, d0, d1);
+                        }
+                        if (grid_meet(p, &sm->s, kBarDown)) make_y(p, &sm->s, sm->step[1].ranges);
+                    }
                 }
             }
         }
@@ -1492,42 +1374,48 @@ namespace {
 
 constexpr uint32_t kSmemLimit = 227 * 1024;
 
+// Stages of an item.  Few pairs: 2, 4 and 8 took 139, 129 and 133 us for a layer
+// of 8 experts of 14336 x 4096 and one token; shorter ones cost more work an
+// item, longer ones leave SMs idle at a step's end.
+constexpr uint32_t kRangeSmall = 4, kRangeLarge = 8;
+
 struct MoePlan {
-    int sms, segs, nt;
     bool small, local;
     int seg;
-    uint32_t range_up, range_down, smem;
-    uint64_t n_cnt, cnt_down, cnt_y;
-    size_t sync, cnt, scores, xp, hi, lo, gu, d, warp_part, cta_part, total;
+    uint32_t range, pool, smem;
+    size_t sync, scores, xp, hi, lo, gu, d, total;
 };
 
 // Workspace parts; the words that have to be zero between calls come first.
-MoePlan plan(const MoeCall &c, int sms) {
+MoePlan plan(const MoeCall &c) {
     MoePlan pl = {};
     const uint64_t slots = static_cast<uint64_t>(c.tokens) * c.top_k;
     const uint64_t H = c.up->cols, F = c.down->cols;
-    pl.sms = sms;
-    // (not by this call's tokens: the counters then lie in the same place for
-    // every call with these containers, and what another call left there is zero)
-    pl.segs = c.experts + moe::kMaxSlots / moe::kSegSmall;
-    // few pairs an expert on average: warps share a row group's columns (one
-    // with more than eight pairs is read once for every eight)
+    // few pairs an expert on average (one with more than eight is read once
+    // for every eight), or many
     pl.small = slots <= 4ull * c.experts || c.tokens <= 8;
     pl.seg = pl.small ? moe::kSegSmall : moe::kSegLarge;
-    const uint32_t fixed = 1024 + moe::kRingBytes + align_up(sizeof(moe::SmallShared), 16);
-    const uint64_t x_bytes = 2ull * c.tokens * H;
-    // little enough for every CTA to do alone: less time than a meeting of the grid
-    pl.local = pl.small && fixed + x_bytes <= kSmemLimit && c.tokens * c.experts <= 512 &&
-               (c.ids_in || static_cast<uint64_t>(c.tokens) * c.experts * H <= (1u << 18));
-    pl.smem = pl.small ? fixed + static_cast<uint32_t>(pl.local ? x_bytes : 0)
-                       : 1024 + moe::kRingBytes + moe::kWarps * 2 * moe::kPartBytes + sizeof(moe::Shared);
-    pl.range_up = pl.range_down = 4;
-    const uint64_t g_up = 2 * F / 16, g_down = H / 16;
-    pl.cnt_down = pl.segs * g_up;
-    pl.cnt_y = pl.cnt_down + pl.segs * g_down;
-    pl.n_cnt = pl.cnt_y + g_down;
-    const int most = static_cast<int>(std::min<uint64_t>(slots, pl.seg));  // pairs of a segment
-    pl.nt = most <= 8 ? 1 : most <= 16 ? 2 : most <= 32 ? 4 : 8;
+    pl.range = pl.small ? kRangeSmall : kRangeLarge;
+    if (pl.small) {
+        const uint32_t fixed = 1024 + moe::kRingBytes + align_up(sizeof(moe::SmallShared), 16);
+        const uint64_t x_bytes = 2ull * c.tokens * H;
+        // little enough for every CTA to do alone: less time than a meeting of the grid
+        pl.local = fixed + x_bytes <= kSmemLimit && c.tokens * c.experts <= 512 &&
+                   (c.ids_in || static_cast<uint64_t>(c.tokens) * c.experts * H <= (1u << 18));
+        pl.smem = fixed + static_cast<uint32_t>(pl.local ? x_bytes : 0);
+    } else {
+        const uint32_t fixed = 1024 + moe::kLargeRingBytes + align_up(sizeof(moe::LargeShared), 128);
+        pl.pool = kSmemLimit - fixed;
+        pl.smem = kSmemLimit;
+        static_assert(kSmemLimit - 1024 - moe::kLargeRingBytes - sizeof(moe::LargeShared) - 128 >=
+                          2 * (2 * 256 * moe::kSegLarge + 64),
+                      "x of a stage fits beside the rings");
+    }
+    // (by the shorter ranges always: a call of fewer tokens never needs more)
+    const auto ranges = [](uint64_t cols) {
+        const uint64_t stages = (cols / kTile + stage::kNT - 1) / stage::kNT;
+        return (stages + kRangeSmall - 1) / kRangeSmall;
+    };
     size_t at = 0;
     auto take = [&](uint64_t bytes) {
         const size_t o = at;
@@ -1535,18 +1423,12 @@ MoePlan plan(const MoeCall &c, int sms) {
         return o;
     };
     pl.sync = take(moe::kSyncWords * 4);
-    pl.cnt = take(pl.n_cnt * 4);
     pl.scores = take(8ull * c.tokens * c.experts);
-    pl.xp = take(2ull * c.tokens * H);
+    pl.xp = take(2 * slots * H);
     pl.hi = take(2 * slots * F);
     pl.lo = take(2 * slots * F);
-    const auto ranges = [&](uint64_t cols, uint32_t stages) {
-        return pl.small ? ((cols / kTile + stage::kNT - 1) / stage::kNT + stages - 1) / stages : 1;
-    };
-    pl.gu = take(pl.small ? 4 * slots * 2 * F * ranges(H, pl.range_up) : 0);
-    pl.d = take(4 * slots * H * ranges(F, pl.range_down));
-    pl.warp_part = take(pl.nt == 1 ? 0 : static_cast<uint64_t>(sms) * moe::kWarps * 2 * pl.nt * moe::kPartBytes);
-    pl.cta_part = take(static_cast<uint64_t>(sms) * 2 * pl.nt * moe::kPartBytes);
+    pl.gu = take(4 * slots * 2 * F * ranges(H));
+    pl.d = take(4 * slots * H * ranges(F));
     pl.total = at;
     return pl;
 }
@@ -1569,16 +1451,12 @@ int fill_mat(moe::Mat &m, const s12_view *v, int rows_e) {
 
 }  // namespace
 
-size_t moe_ws_bytes(const MoeCall &c) {
-    int sms = 0;
-    if (device_sms(&sms) != cudaSuccess) return 0;
-    return plan(c, sms).total;
-}
+size_t moe_ws_bytes(const MoeCall &c) { return plan(c).total; }
 
 int launch_moe(const MoeCall &c, void *ws, size_t ws_bytes, cudaStream_t stream) {
     int sms = 0;
     if (device_sms(&sms) != cudaSuccess) return S12_ERR_CUDA;
-    const MoePlan pl = plan(c, sms);
+    const MoePlan pl = plan(c);
     if (ws_bytes < pl.total) return S12_ERR_CAPACITY;
     moe::Params p = {};
     p.H = static_cast<int>(c.up->cols);
@@ -1599,33 +1477,27 @@ int launch_moe(const MoeCall &c, void *ws, size_t ws_bytes, cudaStream_t stream)
     p.top_k = c.top_k;
     p.renorm = c.renorm;
     p.y_f32 = c.y_type == S12_TYPE_F32;
+    p.seg = pl.seg;
+    p.local = pl.local;
+    p.range = pl.range;
+    p.pool = pl.pool;
     uint8_t *w = static_cast<uint8_t *>(ws);
     p.sync = reinterpret_cast<uint32_t *>(w + pl.sync);
-    p.cnt = reinterpret_cast<uint32_t *>(w + pl.cnt);
-    p.n_cnt = static_cast<uint32_t>(pl.n_cnt);
-    p.cnt_down = static_cast<uint32_t>(pl.cnt_down);
-    p.cnt_y = static_cast<uint32_t>(pl.cnt_y);
     p.scores = reinterpret_cast<double *>(w + pl.scores);
     p.xp = w + pl.xp;
     p.hi = w + pl.hi;
     p.lo = w + pl.lo;
     p.gu = reinterpret_cast<float *>(w + pl.gu);
     p.d = reinterpret_cast<float *>(w + pl.d);
-    p.warp_part = reinterpret_cast<float *>(w + pl.warp_part);
-    p.cta_part = reinterpret_cast<float *>(w + pl.cta_part);
-    p.local = pl.local;
-    p.seg = pl.seg;
-    p.range_up = pl.range_up;
-    p.range_down = pl.range_down;
-    const uint32_t smem = pl.smem;
-    auto kern = pl.small ? (c.up->version == 1 ? moe::moe_small_kernel<1> : moe::moe_small_kernel<2>)
-                         : (c.up->version == 1 ? moe::moe_kernel<1> : moe::moe_kernel<2>);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    const bool v1 = c.up->version == 1;
+    auto kern = pl.small ? (v1 ? moe::moe_small_kernel<1> : moe::moe_small_kernel<2>)
+                         : (v1 ? moe::moe_large_kernel<1> : moe::moe_large_kernel<2>);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem) != cudaSuccess)
         return S12_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sms);
-    cfg.blockDim = dim3(moe::kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(pl.small ? moe::kThreads : moe::kLargeThreads);
+    cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs meet, so all have to be resident

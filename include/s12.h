@@ -419,13 +419,10 @@ size_t s12_moe_ws_bytes(const s12_view *gate_up, const s12_view *down, int exper
  *   ids, weights: device int32 and FP32, tokens x top_k, or NULL: the chosen
  *            experts, largest score first, and their weights.
  *   ws:      device workspace of s12_moe_ws_bytes bytes (else
- *            S12_ERR_CAPACITY), ZERO-FILLED before its first use and usable
- *            again by any later call with containers and experts of the same
- *            shapes (another layer's, say) for which it is large enough,
- *            captured in a graph or not.  Calls of other shapes place its
- *            parts elsewhere: they need a workspace of their own, or a zero
- *            fill between.  Calls that may run at the same time need
- *            different workspaces.
+ *            S12_ERR_CAPACITY), ZERO-FILLED before its first use.  Calls of
+ *            any shapes for which it is large enough may use it one after
+ *            the other, captured in a graph or not.  Calls that may run at
+ *            the same time need different workspaces.
  * The scores are sums in 64 bits.  The products accumulate in FP32 and the
  * hidden values are held as the sum of two BF16 values, so y is within 1e-3
  * of the sum of its terms' magnitudes before its own rounding, as in

@@ -119,6 +119,19 @@ def test_moe_small_and_odd_shapes(s12, T, E, k, H, F):
     assert int(ws[:256].to(torch.int32).sum()) == 0
 
 
+def test_one_workspace_for_calls_of_any_shape(s12):
+    """Only the first words have to be zero: layers of other shapes may use the workspace in turn."""
+    cases = [(Layer(s12, E, H, F, E), T, k) for T, E, k, H, F in ((64, 4, 2, 384, 256), (1, 8, 2, 256, 640),
+                                                                  (9, 40, 3, 128, 128), (33, 2, 1, 512, 128))]
+    need = max(s12.s12_moe_ws_bytes(*L.views, L.E, T, k) for L, T, k in cases)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for L, T, k in cases:
+            x = L.tokens(T, k)
+            y, ids, w = s12.s12_moe(*L.views, L.E, x, L.router, k, ws=ws)
+            check(y, *reference(L, x, *choose(L, x, k, True)))
+
+
 @pytest.mark.parametrize("version", [1, 2])
 @pytest.mark.parametrize("outliers,zeros", [(0.0, 0.0), (0.05, 0.0), (0.3, 0.1), (0.001, 0.5)])
 def test_moe_escapes_and_container_versions(s12, version, outliers, zeros):
@@ -321,13 +334,15 @@ def test_no_tokens_and_binding_refusals(s12):
                            torch.zeros(3, 3, device="cuda"))
 
 
-@pytest.mark.parametrize("T", [1, 64])
-def test_moe_full_size_block(s12, T):
-    """The 8-expert block of the benchmark, top 2."""
-    L = Layer(s12, 8, 4096, 14336, 37, outliers=0.0005)
+@pytest.mark.parametrize("T,E,k,H,F", [(1, 8, 2, 4096, 14336), (64, 8, 2, 4096, 14336), (64, 32, 4, 2176, 1408),
+                                       (9, 32, 4, 2176, 1408), (40, 64, 8, 2048, 1024)])
+def test_moe_full_size_block(s12, T, E, k, H, F):
+    """The 8-expert block of the benchmark, top 2; many smaller experts, whose last rows leave warps without a row
+    group while column ranges of one stage follow one another."""
+    L = Layer(s12, E, H, F, 37, outliers=0.0005)
     x, flag = L.tokens(T, 1), new_flag()
-    y, ids, w = s12.s12_moe(*L.views, 8, x, L.router, 2, err_flag=flag)
-    want, weights = choose(L, x, 2, True)
+    y, ids, w = s12.s12_moe(*L.views, E, x, L.router, k, err_flag=flag)
+    want, weights = choose(L, x, k, True)
     assert np.array_equal(ids.cpu().numpy(), want)
     check(y, *reference(L, x, want, weights))
     assert int(flag.item()) == 0
