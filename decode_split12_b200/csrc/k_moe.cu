@@ -108,11 +108,10 @@ struct Shared {
     unsigned long long bars[kWarps * kStages];
     float weight[kMaxSlots];
     int16_t expert[kMaxSlots];  // of each (token, slot), -1 for none
-    uint16_t list[kMaxSlots];   // (token, slot) pairs by expert
-    uint16_t token[kMaxSlots];  // of each of them
+    uint16_t token[kMaxSlots];  // of each pair of the list: the (token, slot) pairs by expert
     uint16_t place[kMaxSlots];  // of each (token, slot) in the list
     uint16_t segment[kMaxSlots];  // of each of the list
-    int count[S12_MOE_MAX_EXPERTS], first[S12_MOE_MAX_EXPERTS];
+    int count[S12_MOE_MAX_EXPERTS], first[S12_MOE_MAX_EXPERTS], next[S12_MOE_MAX_EXPERTS];
     uint16_t seg_expert[kMaxSegs], seg_first[kMaxSegs];
     uint8_t seg_n[kMaxSegs];
     int n_segs, most;  // segments; pairs of the largest
@@ -222,25 +221,41 @@ __device__ __forceinline__ void score(const Params &p, double *scores, int u0, i
         for (int i = 0; i < TT; ++i)
 #pragma unroll
             for (int j = 0; j < TE; ++j) acc[i][j] = 0.0;
-#pragma unroll(TT == 1 ? 8 : 1)
-        for (int k = lane * 8; k < p.H; k += 256) {
-            float xv[TT][8];
+        constexpr int kBatch = TT == 1 ? 8 : 1;  // loads in flight
+        for (int k0 = lane * 8; k0 < p.H; k0 += 256 * kBatch) {
+            uint4 xr[kBatch][TT], rr[kBatch][TE];
 #pragma unroll
-            for (int i = 0; i < TT; ++i) {
-                const size_t t = min(t0 + i, p.tokens - 1);
-                unpack8(__ldg(reinterpret_cast<const uint4 *>(p.x + t * p.H + k)), xv[i]);
-            }
-#pragma unroll
-            for (int j = 0; j < TE; ++j) {
-                const size_t e = min(e0 + j, p.experts - 1);
-                float rv[8];
-                unpack8(__ldg(reinterpret_cast<const uint4 *>(p.router + e * p.H + k)), rv);
+            for (int b = 0; b < kBatch; ++b) {
+                const int k = k0 + 256 * b;
 #pragma unroll
                 for (int i = 0; i < TT; ++i) {
-                    float s = xv[i][0] * rv[0];
+                    const size_t t = min(t0 + i, p.tokens - 1);
+                    xr[b][i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (k < p.H) xr[b][i] = __ldg(reinterpret_cast<const uint4 *>(p.x + t * p.H + k));
+                }
 #pragma unroll
-                    for (int c = 1; c < 8; ++c) s = fmaf(xv[i][c], rv[c], s);
-                    acc[i][j] += static_cast<double>(s);
+                for (int j = 0; j < TE; ++j) {
+                    const size_t e = min(e0 + j, p.experts - 1);
+                    rr[b][j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (k < p.H) rr[b][j] = __ldg(reinterpret_cast<const uint4 *>(p.router + e * p.H + k));
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                float xv[TT][8];
+#pragma unroll
+                for (int i = 0; i < TT; ++i) unpack8(xr[b][i], xv[i]);
+#pragma unroll
+                for (int j = 0; j < TE; ++j) {
+                    float rv[8];
+                    unpack8(rr[b][j], rv);
+#pragma unroll
+                    for (int i = 0; i < TT; ++i) {
+                        float s = xv[i][0] * rv[0];
+#pragma unroll
+                        for (int c = 1; c < 8; ++c) s = fmaf(xv[i][c], rv[c], s);
+                        acc[i][j] += static_cast<double>(s);
+                    }
                 }
             }
         }
@@ -265,44 +280,46 @@ __device__ __forceinline__ void select_experts(const Params &p, Shared *sm, cons
     const int lane = threadIdx.x & 31;
     const double *row = scores + static_cast<size_t>(t) * p.experts;
     const double low = -__longlong_as_double(0x7FF0000000000000ll);
+    // scores as integers of the same order, 0 for an expert that is chosen or not there
+    unsigned long long key[kPer];
     double v[kPer];
-    uint32_t left = 0u;  // bit i: expert lane + 32 i is not chosen yet
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
+        key[i] = 0;
         v[i] = low;
+        if (32 * i >= p.experts) continue;
+        const int e = lane + 32 * i;
         if (e < p.experts) {
             v[i] = row[e];
             if (v[i] != v[i]) v[i] = low;
-            left |= 1u << i;
+            const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v[i] + 0.0));
+            key[i] = b >> 63 ? ~b : b | 1ull << 63;  // (-infinity: 2^52 - 1)
         }
     }
     double top = 0.0;
     float mine = 0.f;  // lane s < top_k: the weight of slot s before its division
     int chosen = -1;
     for (int s = 0; s < p.top_k; ++s) {
-        double best = low;
+        unsigned long long best = 0;
         int at = 0x7FFFFFFF;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if ((left >> i & 1u) && (at == 0x7FFFFFFF || v[i] > best)) {
-                best = v[i];
+            if (32 * i < p.experts && key[i] > best) {
+                best = key[i];
                 at = lane + 32 * i;
             }
+        const uint32_t hi = static_cast<uint32_t>(best >> 32), most = __reduce_max_sync(0xFFFFFFFFu, hi);
+        const uint32_t lo = hi == most ? static_cast<uint32_t>(best) : 0u, least = __reduce_max_sync(0xFFFFFFFFu, lo);
+        at = __reduce_min_sync(0xFFFFFFFFu, hi == most && lo == least && best ? at : 0x7FFFFFFF);
+        const unsigned long long k = (static_cast<unsigned long long>(most) << 32) | least;
+        const double value = __longlong_as_double(static_cast<long long>(k >> 63 ? k & ~(1ull << 63) : ~k));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const double b = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-            const int a = __shfl_xor_sync(0xFFFFFFFFu, at, o);
-            if (a != 0x7FFFFFFF && (at == 0x7FFFFFFF || b > best || (b == best && a < at))) {
-                best = b;
-                at = a;
-            }
-        }
-        if ((at & 31) == lane) left &= ~(1u << (at >> 5));
-        if (s == 0) top = best;
+        for (int i = 0; i < kPer; ++i)
+            if (at == lane + 32 * i) key[i] = 0;
+        if (s == 0) top = value;
         if (lane == s) {
             chosen = at;
-            mine = expf(static_cast<float>(best - top));
+            mine = expf(static_cast<float>(value - top));
         }
     }
     float sum = 0.f;
@@ -311,7 +328,7 @@ __device__ __forceinline__ void select_experts(const Params &p, Shared *sm, cons
     } else {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i < p.experts) sum += expf(static_cast<float>(v[i] - top));
+            if (32 * i < p.experts && lane + 32 * i < p.experts) sum += expf(static_cast<float>(v[i] - top));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -339,12 +356,10 @@ __device__ __forceinline__ void route(const Params &p, Shared *sm, const double 
     } else {
         for (int t = tid >> 5; t < p.tokens; t += blockDim.x >> 5) select_experts(p, sm, scores, t);
     }
+    for (int e = tid; e < p.experts; e += blockDim.x) sm->count[e] = 0;
     __syncthreads();
-    if (tid < p.experts) {
-        int n = 0;
-        for (int i = 0; i < slots; ++i) n += sm->expert[i] == tid;
-        sm->count[tid] = n;
-    }
+    for (int i = tid; i < slots; i += blockDim.x)
+        if (sm->expert[i] >= 0) atomicAdd(&sm->count[sm->expert[i]], 1);
     __syncthreads();
     if (tid < 32) {
         constexpr int kPer = S12_MOE_MAX_EXPERTS / 32;
@@ -369,8 +384,8 @@ __device__ __forceinline__ void route(const Params &p, Shared *sm, const double 
         for (int i = 0; i < kPer; ++i) {
             const int e = tid * kPer + i, n = e < p.experts ? sm->count[e] : 0;
             if (e < p.experts) {
-                sm->first[e] = at;
-                sm->count[e] = n ? seg : -1;  // (from here on the expert's first segment)
+                sm->first[e] = sm->next[e] = at;
+                sm->count[e] = seg;  // (from here on the expert's first segment)
             }
             for (int k = 0; k < n; k += p.seg, ++seg) {
                 sm->seg_expert[seg] = static_cast<uint16_t>(e);
@@ -386,16 +401,23 @@ __device__ __forceinline__ void route(const Params &p, Shared *sm, const double 
         }
     }
     __syncthreads();
-    if (tid < p.experts && sm->count[tid] >= 0) {
-        const int first = sm->first[tid], seg = sm->count[tid];
-        int at = first;
-        for (int i = 0; i < slots; ++i)
-            if (sm->expert[i] == tid) {
-                sm->segment[at] = static_cast<uint16_t>(seg + (at - first) / p.seg);
+    if (tid < 32) {
+        // 32 slots at a time, in order: those of one expert follow one another
+        for (int i0 = 0; i0 < slots; i0 += 32) {
+            const int i = i0 + tid, e = i < slots ? sm->expert[i] : -1;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+            const int rank = __popc(same & ((1u << tid) - 1u));
+            int at = 0;
+            if (e >= 0) at = sm->next[e] + rank;
+            __syncwarp();
+            if (e >= 0) {
+                if (rank == 0) sm->next[e] = at + __popc(same);
                 sm->place[i] = static_cast<uint16_t>(at);
                 sm->token[at] = static_cast<uint16_t>(i / p.top_k);
-                sm->list[at++] = static_cast<uint16_t>(i);
+                sm->segment[at] = static_cast<uint16_t>(sm->count[e] + (at - sm->first[e]) / p.seg);
             }
+            __syncwarp();
+        }
     }
     __syncthreads();
 }
@@ -446,16 +468,18 @@ __device__ __forceinline__ void decode_pairs(uint32_t R0, uint32_t R1, uint32_t 
 }
 
 // The exact values of the escapes among 16 decoded weights (code words C),
-// stream index idx on; reads at or past `limit` are skipped and flagged.
-__device__ __forceinline__ void patch(uint32_t (&w)[8], uint2 C, uint32_t idx, uint32_t limit,
-                                      const uint16_t *__restrict__ esc, uint32_t *err) {
+// stream index idx on; reads at or past `limit` are skipped and flagged.  `ev`
+// is the value at index `known`, which was read ahead: most tile rows with
+// escapes have one, and it comes from far away.
+__device__ __forceinline__ void patch(uint32_t (&w)[8], uint2 C, uint32_t idx, uint32_t limit, uint32_t known,
+                                      uint32_t ev, const uint16_t *__restrict__ esc, uint32_t *err) {
     uint64_t mm = (static_cast<uint64_t>(escape_nibbles(C.y)) << 32) | escape_nibbles(C.x);
     while (mm) {
         const int j = (__ffsll(static_cast<long long>(mm)) - 1) >> 2;
         mm &= mm - 1;
         uint32_t v = 0;
         if (idx < limit)
-            v = __ldg(esc + idx);
+            v = idx == known ? ev : __ldg(esc + idx);
         else
             raise_flag(err, S12_FLAG_ESC_RANGE);
         ++idx;
@@ -630,12 +654,13 @@ __device__ __forceinline__ void issue_at(const Params &p, Ring &r, const Desc &d
 // 16), as loaded words.
 struct Words {
     uint32_t w0, w1, w2;  // version 1: base, esc_off[t], esc_off[t + 1]; version 2: tmeta[t]
+    uint32_t ev;          // version 1: the tile row's first escape (read_ahead)
 };
 
 template <int V>
 __device__ __forceinline__ Words load_words(const Mat &m, const Desc &d) {
     const int lane = threadIdx.x & 31, t = d.j + (lane >> 4);
-    Words w = {0u, 0u, 0u};
+    Words w = {0u, 0u, 0u, 0u};
     if (d.live && t < m.T) {
         const size_t at = (static_cast<size_t>(d.row16) * kRowsPerGroup + (lane & 15)) * m.T + t;
         if (V == 1) {
@@ -647,6 +672,13 @@ __device__ __forceinline__ Words load_words(const Mat &m, const Desc &d) {
         }
     }
     return w;
+}
+
+// The first escape of each tile row, a stage ahead of its use and a stage after
+// the words that say where it is.
+template <int V>
+__device__ __forceinline__ void read_ahead(const Mat &m, Words &w) {
+    if (V == 1 && w.w1 != w.w2 && w.w1 < m.n_esc) w.ev = __ldg(m.esc + w.w1);
 }
 
 // The products of one stage: the decoded weights of each 16-column chunk and
@@ -664,74 +696,69 @@ __device__ __forceinline__ void stage_products(const Params &p, const Mat &m, co
     const uint32_t B2A = __shfl_sync(0xFFFFFFFFu, own, src) * 0x00800080u;
     const uint32_t B2B = __shfl_sync(0xFFFFFFFFu, own, src + 8) * 0x00800080u;
     const bool anyesc = __any_sync(0xFFFFFFFFu, V == 1 ? wd.w1 != wd.w2 : wd.w0 >> 8 != 0u);
-    if (!anyesc) {
-        const uint4 cA0 = lds128(oC + (((2u * qh) ^ csw) << 4)), cA1 = lds128(oC + (((2u * qh + 1u) ^ csw) << 4));
-        const uint4 cB0 = lds128(oC + (((2u * qh) ^ csw) << 4) + 1024);
-        const uint4 cB1 = lds128(oC + (((2u * qh + 1u) ^ csw) << 4) + 1024);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint4 rA = lds128(oR + (((4u * qh + c) ^ rsw) << 4));
-            const uint4 rB = lds128(oR + (((4u * qh + c) ^ rsw) << 4) + 2048);
-            if (c == 3) refill();
-            const uint4 kA = c < 2 ? cA0 : cA1, kB = c < 2 ? cB0 : cB1;
-            uint32_t wa[8], wb[8];
-            decode_pairs(rA.x, rA.y, c & 1 ? kA.z : kA.x, B2A, wa);
-            decode_pairs(rA.z, rA.w, c & 1 ? kA.w : kA.y, B2A, wa + 4);
-            decode_pairs(rB.x, rB.y, c & 1 ? kB.z : kB.x, B2B, wb);
-            decode_pairs(rB.z, rB.w, c & 1 ? kB.w : kB.y, B2B, wb + 4);
-            multiply(c, wa, wb);
+    const uint4 cA0 = lds128(oC + (((2u * qh) ^ csw) << 4)), cA1 = lds128(oC + (((2u * qh + 1u) ^ csw) << 4));
+    const uint4 cB0 = lds128(oC + (((2u * qh) ^ csw) << 4) + 1024);
+    const uint4 cB1 = lds128(oC + (((2u * qh + 1u) ^ csw) << 4) + 1024);
+    // escapes of the lane's two tile rows: counts by chunk, stream indexes
+    uint32_t nA = 0, nB = 0, iA = 0, iB = 0, limA = 0, limB = 0, knownA = ~0u, knownB = ~0u, evA = 0, evB = 0;
+    if (anyesc) {
+        // (a lane's first half of a tile row counts from the span's start, the
+        // second half back from its end)
+        uint32_t sA, eA, sB, eB;
+        if (V == 1) {
+            sA = __shfl_sync(0xFFFFFFFFu, wd.w1, src);
+            eA = __shfl_sync(0xFFFFFFFFu, wd.w2, src);
+            sB = __shfl_sync(0xFFFFFFFFu, wd.w1, src + 8);
+            eB = __shfl_sync(0xFFFFFFFFu, wd.w2, src + 8);
+            evA = __shfl_sync(0xFFFFFFFFu, wd.ev, src);
+            evB = __shfl_sync(0xFFFFFFFFu, wd.ev, src + 8);
+            knownA = sA;
+            knownB = sB;
+        } else {
+            // row_esc and the counts of the row's earlier tiles
+            const int r = static_cast<int>(d.row16) * kRowsPerGroup + g;
+            const uint32_t n = wd.w0 >> 8;
+            sA = __ldg(m.off + r) + prefix_count_v2(m, r, d.j, q);
+            sB = __ldg(m.off + r + 8) + prefix_count_v2(m, r + 8, d.j, q);
+            const uint32_t mA = __shfl_sync(0xFFFFFFFFu, n, g), mB = __shfl_sync(0xFFFFFFFFu, n, g + 8);
+            sA += tq ? mA : 0u;
+            sB += tq ? mB : 0u;
+            eA = sA + __shfl_sync(0xFFFFFFFFu, n, src);
+            eB = sB + __shfl_sync(0xFFFFFFFFu, n, src + 8);
         }
-        return;
+        if (sA != eA) nA = chunk_counts(cA0, cA1);
+        if (sB != eB) nB = chunk_counts(cB0, cB1);
+        const uint32_t allA = (nA * 0x01010101u) >> 24, allB = (nB * 0x01010101u) >> 24;
+        const uint32_t pairA = allA + __shfl_xor_sync(0xFFFFFFFFu, allA, 1);
+        const uint32_t pairB = allB + __shfl_xor_sync(0xFFFFFFFFu, allB, 1);
+        if (p.err && d.j + tq < m.T && qh == 0 && (pairA != eA - sA || pairB != eB - sB))
+            raise_flag(p.err, S12_FLAG_ESC_COUNT);
+        iA = qh ? eA - allA : sA;
+        iB = qh ? eB - allB : sB;
+        limA = sA <= eA ? min(eA, m.n_esc) : 0u;
+        limB = sB <= eB ? min(eB, m.n_esc) : 0u;
     }
-    // some row of the stage has escapes: a compact loop.  A lane's first half of
-    // a tile row counts from the span's start, the second half back from its end.
-    uint32_t sA, eA, sB, eB;
-    if (V == 1) {
-        sA = __shfl_sync(0xFFFFFFFFu, wd.w1, src);
-        eA = __shfl_sync(0xFFFFFFFFu, wd.w2, src);
-        sB = __shfl_sync(0xFFFFFFFFu, wd.w1, src + 8);
-        eB = __shfl_sync(0xFFFFFFFFu, wd.w2, src + 8);
-    } else {
-        // row_esc and the counts of the row's earlier tiles
-        const int r = static_cast<int>(d.row16) * kRowsPerGroup + g;
-        const uint32_t n = wd.w0 >> 8;
-        sA = __ldg(m.off + r) + prefix_count_v2(m, r, d.j, q);
-        sB = __ldg(m.off + r + 8) + prefix_count_v2(m, r + 8, d.j, q);
-        const uint32_t nA = __shfl_sync(0xFFFFFFFFu, n, g), nB = __shfl_sync(0xFFFFFFFFu, n, g + 8);
-        sA += tq ? nA : 0u;
-        sB += tq ? nB : 0u;
-        eA = sA + __shfl_sync(0xFFFFFFFFu, n, src);
-        eB = sB + __shfl_sync(0xFFFFFFFFu, n, src + 8);
-    }
-    const uint32_t nA = chunk_counts(lds128(oC + (((2u * qh) ^ csw) << 4)), lds128(oC + (((2u * qh + 1u) ^ csw) << 4)));
-    const uint32_t nB = chunk_counts(lds128(oC + (((2u * qh) ^ csw) << 4) + 1024),
-                                     lds128(oC + (((2u * qh + 1u) ^ csw) << 4) + 1024));
-    const uint32_t allA = (nA * 0x01010101u) >> 24, allB = (nB * 0x01010101u) >> 24;
-    const uint32_t pairA = allA + __shfl_xor_sync(0xFFFFFFFFu, allA, 1);
-    const uint32_t pairB = allB + __shfl_xor_sync(0xFFFFFFFFu, allB, 1);
-    if (p.err && d.j + tq < m.T && qh == 0 && (pairA != eA - sA || pairB != eB - sB))
-        raise_flag(p.err, S12_FLAG_ESC_COUNT);
-    uint32_t iA = qh ? eA - allA : sA, iB = qh ? eB - allB : sB;
-    const uint32_t limA = sA <= eA ? min(eA, m.n_esc) : 0u, limB = sB <= eB ? min(eB, m.n_esc) : 0u;
-#pragma unroll 1
+    const bool patches = __any_sync(0xFFFFFFFFu, (nA | nB) != 0u);
+#pragma unroll
     for (int c = 0; c < 4; ++c) {
         const uint4 rA = lds128(oR + (((4u * qh + c) ^ rsw) << 4));
         const uint4 rB = lds128(oR + (((4u * qh + c) ^ rsw) << 4) + 2048);
-        const uint32_t piece = oC + (((2u * qh + (c >> 1)) ^ csw) << 4) + 8u * (c & 1);
-        const uint2 kA = lds64(piece), kB = lds64(piece + 1024);
+        if (c == 3) refill();
+        const uint4 kA = c < 2 ? cA0 : cA1, kB = c < 2 ? cB0 : cB1;
         uint32_t wa[8], wb[8];
-        decode_pairs(rA.x, rA.y, kA.x, B2A, wa);
-        decode_pairs(rA.z, rA.w, kA.y, B2A, wa + 4);
-        decode_pairs(rB.x, rB.y, kB.x, B2B, wb);
-        decode_pairs(rB.z, rB.w, kB.y, B2B, wb + 4);
-        const uint32_t hereA = (nA >> (8 * c)) & 0xFFu, hereB = (nB >> (8 * c)) & 0xFFu;
-        if (hereA) patch(wa, kA, iA, limA, m.esc, p.err);
-        if (hereB) patch(wb, kB, iB, limB, m.esc, p.err);
-        iA += hereA;
-        iB += hereB;
+        decode_pairs(rA.x, rA.y, c & 1 ? kA.z : kA.x, B2A, wa);
+        decode_pairs(rA.z, rA.w, c & 1 ? kA.w : kA.y, B2A, wa + 4);
+        decode_pairs(rB.x, rB.y, c & 1 ? kB.z : kB.x, B2B, wb);
+        decode_pairs(rB.z, rB.w, c & 1 ? kB.w : kB.y, B2B, wb + 4);
+        if (patches) {
+            const uint32_t hereA = (nA >> (8 * c)) & 0xFFu, hereB = (nB >> (8 * c)) & 0xFFu;
+            if (hereA) patch(wa, c & 1 ? make_uint2(kA.z, kA.w) : make_uint2(kA.x, kA.y), iA, limA, knownA, evA, m.esc, p.err);
+            if (hereB) patch(wb, c & 1 ? make_uint2(kB.z, kB.w) : make_uint2(kB.x, kB.y), iB, limB, knownB, evB, m.esc, p.err);
+            iA += hereA;
+            iB += hereB;
+        }
         multiply(c, wa, wb);
     }
-    refill();
 }
 
 // One step by one warp.  d0 and d1 are its first stages (their copies are in
@@ -747,12 +774,13 @@ __device__ __forceinline__ bool small_step(const Params &p, const SmallShared *s
     const size_t rows = static_cast<size_t>(m.G) * kRowsPerGroup;  // of an expert
     float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains of products
     Words w0 = load_words<V>(m, d0);
+    read_ahead<V>(m, w0);
     const uint8_t *xl = nullptr;  // the lane's column of x or h
     float *to = nullptr;          // its places of the item's sums, for pairs 2q and 2q + 1
     int pairs = 0;
     bool fresh = true;
     while (d0.live) {
-        const Words w1 = load_words<V>(m, d1);
+        Words w1 = load_words<V>(m, d1);
         if (fresh) {
             const Item at = item_at<PH>(st, d0.it);
             const int first = sm->s.seg_first[at.seg];
@@ -795,6 +823,7 @@ __device__ __forceinline__ bool small_step(const Params &p, const SmallShared *s
             __syncwarp();
             d2 = feed.next(p, sm);
             if (d2.live) issue_at<PH>(p, rg, d2);
+            read_ahead<V>(m, w1);
         };
         stage_products<V>(p, m, d0, w0, rg.base + slot * kStageBytes, multiply, refill);
         ++rg.consumed;
@@ -819,27 +848,19 @@ __device__ __forceinline__ bool small_step(const Params &p, const SmallShared *s
     return true;
 }
 
-__device__ __forceinline__ void add4(float4 &a, const float4 &b) {
-    a.x += b.x;
-    a.y += b.y;
-    a.z += b.z;
-    a.w += b.w;
-}
-
 __device__ __forceinline__ float4 shfl4(const float4 &v, int from_xor) {
     return make_float4(__shfl_xor_sync(0xFFFFFFFFu, v.x, from_xor), __shfl_xor_sync(0xFFFFFFFFu, v.y, from_xor),
                        __shfl_xor_sync(0xFFFFFFFFu, v.z, from_xor), __shfl_xor_sync(0xFFFFFFFFu, v.w, from_xor));
 }
 
-// The sums of the 16 rows of a pair's row group over its ranges, 4 to a lane (lane & 3);
-// lanes 4 apart add every eighth range, then one another: a fixed order.
+// Four sums over the ranges of their row group, in order.
 __device__ __forceinline__ float4 sum_ranges(const float *src, size_t plane, uint32_t ranges) {
-    const int lane = threadIdx.x & 31;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (uint32_t c = lane >> 2; c < ranges; c += 8)
-        add4(v, __ldcg(reinterpret_cast<const float4 *>(src + c * plane) + (lane & 3)));
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) add4(v, shfl4(v, o));
+#pragma unroll 4
+    for (uint32_t c = 0; c < ranges; ++c) {
+        const float4 t = __ldcg(reinterpret_cast<const float4 *>(src + c * plane));
+        v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
+    }
     return v;
 }
 
@@ -854,66 +875,63 @@ __device__ __forceinline__ int used_pairs(const Shared *sm) {
     return sm->seg_first[last] + sm->seg_n[last];
 }
 
-// h from the sums of step 1: a warp takes one pair's row group at a time.
+// h from the sums of step 1: two lanes for a pair's row group (8 f, one piece).
 __device__ __forceinline__ void make_hidden(const Params &p, const Shared *sm, uint32_t ranges) {
-    const int lane = threadIdx.x & 31, slots = p.tokens * p.top_k;
-    const uint32_t G = static_cast<uint32_t>(p.up.G), warps = blockDim.x >> 5;
-    const int pairs = used_pairs(sm);
+    const int slots = p.tokens * p.top_k;
+    const uint32_t G = static_cast<uint32_t>(p.up.G), n = used_pairs(sm) * G, half = threadIdx.x & 1;
     const size_t rows = static_cast<size_t>(G) * kRowsPerGroup, plane = static_cast<size_t>(slots) * rows;
-    for (uint32_t u = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < pairs * G; u += gridDim.x * warps) {
+    const uint32_t per = blockDim.x / 2;
+    for (uint32_t u0 = blockIdx.x * per; u0 < n; u0 += gridDim.x * per) {
+        const uint32_t u = min(u0 + threadIdx.x / 2, n - 1);  // (lanes past the end do the last one again)
         const uint32_t pos = u / G, grp = u - pos * G;
-        const float4 v = sum_ranges(p.gu + pos * rows + static_cast<size_t>(grp) * kRowsPerGroup, plane, ranges);
-        // lanes 0 and 1: gate rows 0-3 and 4-7; lanes 2 and 3: the up rows
-        const float4 up = shfl4(v, 2);
+        const float *src = p.gu + pos * rows + static_cast<size_t>(grp) * kRowsPerGroup + 4 * half;
+        const float4 gt = sum_ranges(src, plane, ranges), up = sum_ranges(src + 8, plane, ranges);
         auto h = [](float g, float t) { return g / (1.f + expf(-g)) * t; };
-        const float4 a = make_float4(h(v.x, up.x), h(v.y, up.y), h(v.z, up.z), h(v.w, up.w));
+        const float4 a = make_float4(h(gt.x, up.x), h(gt.y, up.y), h(gt.z, up.z), h(gt.w, up.w));
         const float4 b = shfl4(a, 1);
-        if (lane == 0) {
-            // one piece, in the order 0 4 1 5 2 6 3 7
-            const float f[8] = {a.x, b.x, a.y, b.y, a.z, b.z, a.w, b.w};
-            uint32_t hi[4], lo[4];
+        // one piece, in the order 0 4 1 5 2 6 3 7; the first lane stores the
+        // high parts, the second the low ones
+        const float4 l = half ? b : a, r = half ? a : b;
+        const float f[8] = {l.x, r.x, l.y, r.y, l.z, r.z, l.w, r.w};
+        uint32_t v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                hi[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-                const float r0 = f[2 * i] - __uint_as_float(hi[i] << 16);
-                const float r1 = f[2 * i + 1] - __uint_as_float(hi[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+            v[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+            if (half) {
+                const float r0 = f[2 * i] - __uint_as_float(v[i] << 16);
+                const float r1 = f[2 * i + 1] - __uint_as_float(v[i] & 0xFFFF0000u);
                 // (an infinite h has no rest)
-                lo[i] = pack_bf16(fabsf(r0) < 3.4e38f ? r0 : 0.f, fabsf(r1) < 3.4e38f ? r1 : 0.f);
+                v[i] = pack_bf16(fabsf(r0) < 3.4e38f ? r0 : 0.f, fabsf(r1) < 3.4e38f ? r1 : 0.f);
             }
-            const int in = static_cast<int>(grp & 15u);
-            const int seg = sm->segment[pos], first = sm->seg_first[seg];
-            const size_t o = static_cast<size_t>(first) * p.F * 2 +
-                             piece_at(static_cast<int>(grp >> 4), (in >> 1) & 3, in & 1, sm->seg_n[seg],
-                                      static_cast<int>(pos) - first, in >> 3);
-            *reinterpret_cast<uint4 *>(p.hi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(p.lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
+        const int in = static_cast<int>(grp & 15u), seg = sm->segment[pos], first = sm->seg_first[seg];
+        const size_t o = static_cast<size_t>(first) * p.F * 2 + piece_at(static_cast<int>(grp >> 4), (in >> 1) & 3, in & 1,
+                                                                         sm->seg_n[seg], static_cast<int>(pos) - first,
+                                                                         in >> 3);
+        *reinterpret_cast<uint4 *>((half ? p.lo : p.hi) + o) = make_uint4(v[0], v[1], v[2], v[3]);
     }
 }
 
-// y from the sums of step 2: a warp takes 16 values of a token at a time.
+// y from the sums of step 2: a lane for four values of a token.
 __device__ __forceinline__ void make_y(const Params &p, const Shared *sm, uint32_t ranges) {
-    const int lane = threadIdx.x & 31, slots = p.tokens * p.top_k;
-    const uint32_t G = static_cast<uint32_t>(p.down.G), warps = blockDim.x >> 5;
-    const size_t rows = static_cast<size_t>(G) * kRowsPerGroup, plane = static_cast<size_t>(slots) * rows;
-    for (uint32_t u = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < p.tokens * G; u += gridDim.x * warps) {
-        const uint32_t t = u / G, grp = u - t * G;
+    const int slots = p.tokens * p.top_k;
+    const uint32_t per = static_cast<uint32_t>(p.H) / 4, n = p.tokens * per;
+    const size_t rows = static_cast<size_t>(p.H), plane = static_cast<size_t>(slots) * rows;
+    for (uint32_t u = blockIdx.x * blockDim.x + threadIdx.x; u < n; u += gridDim.x * blockDim.x) {
+        const uint32_t t = u / per, c = (u - t * per) * 4;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < p.top_k; ++s) {
             const int i = static_cast<int>(t) * p.top_k + s;
             if (sm->expert[i] < 0) continue;
-            const float4 v = sum_ranges(p.d + sm->place[i] * rows + static_cast<size_t>(grp) * kRowsPerGroup, plane,
-                                        ranges);
+            const float4 v = sum_ranges(p.d + sm->place[i] * rows + c, plane, ranges);
             const float w = sm->weight[i];
             y = make_float4(fmaf(w, v.x, y.x), fmaf(w, v.y, y.y), fmaf(w, v.z, y.z), fmaf(w, v.w, y.w));
         }
-        if (lane < 4) {
-            const size_t o = static_cast<size_t>(t) * p.H + static_cast<size_t>(grp) * kRowsPerGroup + 4 * lane;
-            put_y(p, o, y.x);
-            put_y(p, o + 1, y.y);
-            put_y(p, o + 2, y.z);
-            put_y(p, o + 3, y.w);
-        }
+        const size_t o = static_cast<size_t>(t) * p.H + c;
+        put_y(p, o, y.x);
+        put_y(p, o + 1, y.y);
+        put_y(p, o + 2, y.z);
+        put_y(p, o + 3, y.w);
     }
 }
 
@@ -1170,6 +1188,7 @@ __device__ __forceinline__ bool large_step(const Params &p, LargeShared *sm, uin
     const size_t rows = static_cast<size_t>(m.G) * kRowsPerGroup;  // of an expert
     XRing xr = x_ring<PH>(p, sm, xbase);
     Words w0 = load_words<V>(m, d0);
+    read_ahead<V>(m, w0);
     for (uint32_t ord = 0;; ++ord) {
         const Unit u = unit_at<PH>(p, sm, ord);
         if (u.n == 0) break;
@@ -1199,7 +1218,7 @@ __device__ __forceinline__ bool large_step(const Params &p, LargeShared *sm, uin
                 sm->abort = 1u;
                 return false;
             }
-            const Words w1 = load_words<V>(m, d1);
+            Words w1 = load_words<V>(m, d1);
             Desc d2;
             if (mine) {
                 const bool live = two || tq == 0;  // the lane's tile exists (else zeros from the copy)
@@ -1228,12 +1247,14 @@ __device__ __forceinline__ bool large_step(const Params &p, LargeShared *sm, uin
                     __syncwarp();
                     d2 = feed.next(p, sm);
                     if (d2.live) issue_at<PH>(p, rg, d2);
+                    read_ahead<V>(m, w1);
                 };
                 stage_products<V>(p, m, d0, w0, rg.base + slot * kStageBytes, multiply, refill);
                 ++rg.consumed;
             } else {
                 d2 = feed.next(p, sm);
                 if (d2.live) issue_at<PH>(p, rg, d2);
+                read_ahead<V>(m, w1);
             }
             d0 = d1;
             d1 = d2;
