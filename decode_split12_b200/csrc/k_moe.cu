@@ -512,11 +512,18 @@ __device__ __forceinline__ void load_x(uint32_t (&xw)[8], const uint8_t *src, si
     xw[4] = b.x; xw[5] = b.y; xw[6] = b.z; xw[7] = b.w;
 }
 
-__device__ __forceinline__ void chunk_mma(float (&acc)[4], const uint32_t (&wa)[8], const uint32_t (&wb)[8],
-                                          const uint32_t (&xw)[8]) {
+// The chunk's four products with each of N eights of tokens.  A product waits
+// for the one before it on the same sums, so neighbours have sums of their own:
+// acc[n] over the eights (N > 1), or four chains for one eight.
+template <int N, int A>
+__device__ __forceinline__ void chunk_mma(float (&acc)[A][4], int n0, const uint32_t (&wa)[8], const uint32_t (&wb)[8],
+                                          const uint32_t (&xw)[N][8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        mma16816(acc, wa[2 * i], wb[2 * i], wa[2 * i + 1], wb[2 * i + 1], xw[2 * i], xw[2 * i + 1]);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            mma16816(acc[N == 1 ? i : n0 + n], wa[2 * i], wb[2 * i], wa[2 * i + 1], wb[2 * i + 1], xw[n][2 * i],
+                     xw[n][2 * i + 1]);
 }
 
 // ---------------------------------------------------------------------------
@@ -772,7 +779,7 @@ __device__ __forceinline__ bool small_step(const Params &p, const SmallShared *s
     const int slots = p.tokens * p.top_k;
     uint32_t half = static_cast<uint32_t>(p.tokens) * 32u;  // (of step 2: the segment's pairs)
     const size_t rows = static_cast<size_t>(m.G) * kRowsPerGroup;  // of an expert
-    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains of products
+    float acc[4][4] = {};  // four chains of products
     Words w0 = load_words<V>(m, d0);
     read_ahead<V>(m, w0);
     const uint8_t *xl = nullptr;  // the lane's column of x or h
@@ -808,13 +815,13 @@ __device__ __forceinline__ bool small_step(const Params &p, const SmallShared *s
         Desc d2;
         d2.live = false;
         auto multiply = [&](int c, const uint32_t (&wa)[8], const uint32_t (&wb)[8]) {
-            uint32_t xw[8];
+            uint32_t xw[1][8];
             const uint8_t *src = xl + at + c * chunk_bytes;
-            load_x(xw, src, half, live);
-            chunk_mma(acc[c & 1], wa, wb, xw);
+            load_x(xw[0], src, half, live);
+            chunk_mma(acc, 0, wa, wb, xw);
             if (PH == 2) {
-                load_x(xw, src + lo, half, live);
-                chunk_mma(acc[c & 1], wa, wb, xw);
+                load_x(xw[0], src + lo, half, live);
+                chunk_mma(acc, 0, wa, wb, xw);
             }
         };
         auto refill = [&]() {
@@ -833,11 +840,11 @@ __device__ __forceinline__ bool small_step(const Params &p, const SmallShared *s
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (2 * q + i < pairs) {
-                    __stcg(to + i * rows, acc[0][i] + acc[1][i]);
-                    __stcg(to + i * rows + 8, acc[0][2 + i] + acc[1][2 + i]);
+                    __stcg(to + i * rows, acc[0][i] + acc[1][i] + acc[2][i] + acc[3][i]);
+                    __stcg(to + i * rows + 8, acc[0][2 + i] + acc[1][2 + i] + acc[2][2 + i] + acc[3][2 + i]);
                 }
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
         }
@@ -1022,6 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_small_kernel(const __grid_con
 // its own, x cost three times the weights' traffic to L2.  Units come from a
 // counter of the grid as items do above, claimed by the warp that copies x.
 
+constexpr int kEights = 2;  // eights of tokens that are multiplied side by side
 constexpr int kMaxX = 16;   // places of the x ring
 constexpr int kUnits = 32;  // the queue: copying x is at most kMaxX units ahead of a warp
 
@@ -1226,18 +1234,25 @@ __device__ __forceinline__ bool large_step(const Params &p, LargeShared *sm, uin
                 auto multiply = [&](int c, const uint32_t (&wa)[8], const uint32_t (&wb)[8]) {
                     const uint32_t xc = xl + 2u * c * half;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        if (nt < nts) {
-                            const uint32_t at = xc + (nt + 1 == nts ? off_last : off + 256u * nt);
+                    for (int n0 = 0; n0 < NT; n0 += kEights)
+                        if (n0 < nts) {
 #pragma unroll
                             for (int plane = 0; plane < PH; ++plane) {
-                                uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-                                if (live) {
-                                    a = lds128(at + plane * 8u * half);
-                                    b = lds128(at + plane * 8u * half + half);
+                                uint32_t xw[kEights][8];
+#pragma unroll
+                                for (int n = 0; n < kEights; ++n) {
+                                    // (eights past the last repeat it; their sums are dropped)
+                                    const uint32_t at = xc + plane * 8u * half +
+                                                        (n0 + n + 1 >= nts ? off_last : off + 256u * (n0 + n));
+                                    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+                                    if (live) {
+                                        a = lds128(at);
+                                        b = lds128(at + half);
+                                    }
+                                    xw[n][0] = a.x; xw[n][1] = a.y; xw[n][2] = a.z; xw[n][3] = a.w;
+                                    xw[n][4] = b.x; xw[n][5] = b.y; xw[n][6] = b.z; xw[n][7] = b.w;
                                 }
-                                const uint32_t xw[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                                chunk_mma(acc[nt], wa, wb, xw);
+                                chunk_mma(acc, n0, wa, wb, xw);
                             }
                         }
                 };
