@@ -62,7 +62,7 @@ struct __align__(64) Params {
     int rest, ranges;        // tiles before them, and the workers (from 0) that their stages are dealt to
     long long units;         // those tiles' stages
     uint32_t *err;
-    uint32_t *cnt;           // workspace: one arrival counter per CTA (zero between calls)
+    uint32_t *cnt;           // workspace's head: one arrival counter per CTA (zero between calls)
     int32_t *part;           // workspace: [CTAs][2][tokens][kRows] parts of shared tiles
     int stages;
     uint32_t stage_bytes, acc_cols, tmem_cols;  // of one CTA
@@ -579,9 +579,7 @@ Plan8 plan8(int64_t M, int sms) {
     const int64_t tiles = (M + gemm8::kMaxTokens - 1) / gemm8::kMaxTokens, step = 16 * pl.cg;
     pl.tiles_m = static_cast<int>(tiles);
     pl.tokens = static_cast<int>(((M + tiles - 1) / tiles + step - 1) / step * step);
-    // the counters first and their size by the device alone: calls of other
-    // shapes may use the workspace in turn
-    pl.cnt_bytes = align_up(static_cast<uint64_t>(sms) * 4, kAlign);
+    pl.cnt_bytes = S12_WS_HEAD;  // (a counter for each CTA)
     pl.part_bytes = static_cast<size_t>(sms) * 2 * pl.tokens * gemm8::kRows * 4;
     return pl;
 }
@@ -633,6 +631,7 @@ size_t gemm_i8_ws_bytes(int64_t M) {
 int launch_gemm_i8(const Gemm8Call &c, void *ws, size_t ws_bytes, cudaStream_t stream) {
     int sms = 0;
     if (device_sms(&sms) != cudaSuccess) return S12_ERR_CUDA;
+    if (sms > S12_WS_HEAD / 4) return S12_ERR_DEVICE;
     const Plan8 pl = plan8(c.M, sms);
     if (ws_bytes < pl.cnt_bytes + pl.part_bytes) return S12_ERR_CAPACITY;
     gemm8::Params p = {};

@@ -81,6 +81,7 @@ struct __align__(64) Mat {
 
 // Words that the grid meets at.
 enum { kBarRoute, kBarPack, kBarSums, kBarHidden, kBarDown, kNext1, kNext2, kExits, kAbort, kSyncWords };
+static_assert(kSyncWords * 4 <= S12_WS_HEAD, "they lie in the workspace's head");
 
 struct __align__(64) Params {
     Mat up, down;
@@ -1422,14 +1423,14 @@ struct MoePlan {
     size_t sync, scores, xp, hi, lo, gu, d, total;
 };
 
-// Workspace parts; the words that have to be zero between calls come first.
+// Workspace parts; the words that have to be zero between calls are its head.
 MoePlan plan(const MoeCall &c) {
     MoePlan pl = {};
     const uint64_t slots = static_cast<uint64_t>(c.tokens) * c.top_k;
     const uint64_t H = c.up->cols, F = c.down->cols;
     // few pairs an expert on average (one with more than eight is read once
     // for every eight), or many
-    pl.small = slots <= 4ull * c.experts || c.tokens <= 8;
+    pl.small = slots <= 8ull * c.experts || c.tokens <= 8;
     pl.seg = pl.small ? moe::kSegSmall : moe::kSegLarge;
     pl.range = pl.small ? kRangeSmall : kRangeLarge;
     if (pl.small) {
@@ -1458,7 +1459,7 @@ MoePlan plan(const MoeCall &c) {
         at += align_up(bytes, kAlign);
         return o;
     };
-    pl.sync = take(moe::kSyncWords * 4);
+    pl.sync = take(S12_WS_HEAD);
     pl.scores = take(8ull * c.tokens * c.experts);
     pl.xp = take(2 * slots * H);
     pl.hi = take(2 * slots * F);

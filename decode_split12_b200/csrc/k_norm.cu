@@ -47,7 +47,7 @@ struct Args {
     long long rows;
     int cols;
     float eps;
-    int x_f32, res_f32, normed;
+    int x_f32, res_f32;
 };
 
 __device__ __forceinline__ void unpack(const uint4 &a, float (&v)[kVec]) {
@@ -108,14 +108,23 @@ __device__ __forceinline__ void load_row(const void *base, size_t row0, int cols
     }
 }
 
+// Four values to 8 bits, the nearest integers.
+__device__ __forceinline__ uint32_t to_eight(float a, float b, float c, float d) {
+    uint32_t lo, v;
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(lo) : "r"(__float2int_rn(d)), "r"(__float2int_rn(c)), "r"(0));
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(v) : "r"(__float2int_rn(b)), "r"(__float2int_rn(a)), "r"(lo));
+    return v;
+}
+
 // One row by n threads (t = 0 .. n-1), `reduce` summing ss and taking the
-// largest top over them.
-template <int NV, class Reduce>
+// largest top over them.  PLAIN: the quantiser (x to q and scale, nothing
+// else), which needs fewer registers.
+template <int NV, bool PLAIN, class Reduce>
 __device__ __forceinline__ void do_row(const Args &a, long long row, int t, int n, Reduce reduce) {
     const size_t row0 = static_cast<size_t>(row) * static_cast<size_t>(a.cols);
     float s[NV][kVec];
     load_row<NV>(a.x, row0, a.cols, a.x_f32 != 0, t, n, s);
-    if (a.res) {
+    if (!PLAIN && a.res) {
         float r[NV][kVec];
         load_row<NV>(a.res, row0, a.cols, a.res_f32 != 0, t, n, r);
 #pragma unroll
@@ -123,7 +132,7 @@ __device__ __forceinline__ void do_row(const Args &a, long long row, int t, int 
 #pragma unroll
             for (int k = 0; k < kVec; ++k) s[i][k] += r[i][k];
     }
-    if (a.res_out) {
+    if (!PLAIN && a.res_out) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = t + i * n;
@@ -144,8 +153,8 @@ __device__ __forceinline__ void do_row(const Args &a, long long row, int t, int 
     for (int i = 0; i < NV; ++i) {
         const int c = t + i * n;
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) ss = fmaf(s[i][k], s[i][k], ss);
-        if (a.w && c * kVec < a.cols) {
+        for (int k = 0; k < kVec && !PLAIN; ++k) ss = fmaf(s[i][k], s[i][k], ss);
+        if (!PLAIN && a.w && c * kVec < a.cols) {
             float w[kVec];
             unpack(reinterpret_cast<const uint4 *>(a.w)[c], w);
 #pragma unroll
@@ -157,8 +166,8 @@ __device__ __forceinline__ void do_row(const Args &a, long long row, int t, int 
     reduce(ss, top);
     // (a row of zeros with eps = 0 stays a row of zeros)
     const float ms = ss / static_cast<float>(a.cols) + a.eps;
-    const float f = !a.normed ? 1.f : ms == 0.f ? 0.f : __frsqrt_rn(ms);
-    if (a.y) {
+    const float f = PLAIN ? 1.f : ms == 0.f ? 0.f : __frsqrt_rn(ms);
+    if (!PLAIN && a.y) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = t + i * n;
@@ -170,24 +179,28 @@ __device__ __forceinline__ void do_row(const Args &a, long long row, int t, int 
             }
         }
     }
-    if (a.q) {
+    if (PLAIN || a.q) {
         const bool finite = top < 0x7F800000u;
         // 127 / max|p| overflows for the smallest maxima: those rows are
         // scaled up by 2^64 first (exact: their values are that small)
-        const float up = top < 0x0D000000u ? 18446744073709551616.f : 1.f;
         const float m = __uint_as_float(top);
-        const float g = finite && top ? 127.f / (m * up) : 0.f;
+        float g = finite && top ? 127.f / m : 0.f;
+        if (top < 0x0D000000u) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) s[i][k] *= 18446744073709551616.f;
+            g = top ? 127.f / (m * 18446744073709551616.f) : 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = t + i * n;
             if (c * kVec < a.cols) {
-                uint32_t b[2] = {0u, 0u};
+                float v[kVec];
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) {
-                    const int v = finite ? __float2int_rn(s[i][k] * up * g) : 0;
-                    b[k >> 2] |= (static_cast<uint32_t>(v) & 0xFFu) << (8 * (k & 3));
-                }
-                reinterpret_cast<uint2 *>(a.q + row0)[c] = make_uint2(b[0], b[1]);
+                for (int k = 0; k < kVec; ++k) v[k] = finite ? s[i][k] * g : 0.f;
+                reinterpret_cast<uint2 *>(a.q + row0)[c] =
+                    make_uint2(to_eight(v[0], v[1], v[2], v[3]), to_eight(v[4], v[5], v[6], v[7]));
             }
         }
         if (t == 0) a.scale[row] = finite ? m * f / 127.f : __uint_as_float(0x7FC00000u);
@@ -201,23 +214,23 @@ __device__ __forceinline__ void warp_reduce(float &ss, uint32_t &top) {
 }
 
 // One row to a warp.
-template <int NV>
+template <int NV, bool PLAIN>
 __global__ void __launch_bounds__(32 * kWarpRows) warp_kernel(const Args a) {
     grid_launch_dependents();
     const long long row = static_cast<long long>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5);
     if (row >= a.rows) return;
     grid_dependency_wait();
-    do_row<NV>(a, row, threadIdx.x & 31, 32, [](float &ss, uint32_t &top) { warp_reduce(ss, top); });
+    do_row<NV, PLAIN>(a, row, threadIdx.x & 31, 32, [](float &ss, uint32_t &top) { warp_reduce(ss, top); });
 }
 
-// One row to a block.
-template <int NV>
-__global__ void __launch_bounds__(kMaxThreads) block_kernel(const Args a) {
+// One row to a block of at most THREADS threads, BLOCKS of them on an SM.
+template <int NV, bool PLAIN, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) block_kernel(const Args a) {
     __shared__ float part[32];
     __shared__ uint32_t tops[32];
     grid_launch_dependents();
     grid_dependency_wait();
-    do_row<NV>(a, blockIdx.x, threadIdx.x, blockDim.x, [&](float &ss, uint32_t &top) {
+    do_row<NV, PLAIN>(a, blockIdx.x, threadIdx.x, blockDim.x, [&](float &ss, uint32_t &top) {
         warp_reduce(ss, top);
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
         if (lane == 0) {
@@ -249,11 +262,35 @@ int launch_rows(Kernel kern, unsigned grid, unsigned threads, const norm::Args &
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? S12_OK : S12_ERR_CUDA;
 }
 
+template <bool PLAIN>
+int launch_kind(const norm::Args &a, int sms, cudaStream_t stream) {
+    using namespace norm;
+    const int vecs = a.cols / kVec;
+    if (a.cols <= 32 * kVec * kMaxVecs) {
+        const int nv = (vecs + 31) / 32;
+        const unsigned grid = static_cast<unsigned>((a.rows + kWarpRows - 1) / kWarpRows);
+        if (nv == 1) return launch_rows(warp_kernel<1, PLAIN>, grid, 32 * kWarpRows, a, stream);
+        if (nv == 2) return launch_rows(warp_kernel<2, PLAIN>, grid, 32 * kWarpRows, a, stream);
+        return launch_rows(warp_kernel<4, PLAIN>, grid, 32 * kWarpRows, a, stream);
+    }
+    // Few rows: as many threads as vectors, so that each loads once (one row of
+    // 4096: 2.5 us).  Many rows: four vectors a thread, so that more rows share
+    // an SM (4096 rows of 8192, norm and quantiser: 45 and 24 us, against 49
+    // and 28 with two and 62 and 41 with one).
+    const unsigned grid = static_cast<unsigned>(a.rows);
+    const bool few = a.rows <= 2 * sms;
+    const int nv = few && vecs <= kMaxThreads ? 1 : few && vecs <= 2 * kMaxThreads ? 2 : 4;
+    const unsigned threads = static_cast<unsigned>(((vecs + nv - 1) / nv + 31) / 32 * 32);
+    if (nv == 1) return launch_rows(block_kernel<1, PLAIN, kMaxThreads, 1>, grid, threads, a, stream);
+    if (nv == 2) return launch_rows(block_kernel<2, PLAIN, kMaxThreads, 1>, grid, threads, a, stream);
+    if (threads <= 256) return launch_rows(block_kernel<4, PLAIN, 256, PLAIN ? 6 : 4>, grid, threads, a, stream);
+    return launch_rows(block_kernel<4, PLAIN, kMaxThreads, 1>, grid, threads, a, stream);
+}
+
 }  // namespace
 
 int launch_norm(const NormCall &c, cudaStream_t stream) {
-    using namespace norm;
-    Args a = {};
+    norm::Args a = {};
     a.x = c.x;
     a.res = c.residual;
     a.res_out = c.residual_out;
@@ -266,27 +303,9 @@ int launch_norm(const NormCall &c, cudaStream_t stream) {
     a.eps = c.eps;
     a.x_f32 = c.x_type == S12_TYPE_F32;
     a.res_f32 = c.residual_type == S12_TYPE_F32;
-    a.normed = c.normed;
-    const int vecs = a.cols / kVec;
-    if (a.cols <= 32 * kVec * kMaxVecs) {
-        const int nv = (vecs + 31) / 32;
-        const unsigned grid = static_cast<unsigned>((c.rows + kWarpRows - 1) / kWarpRows);
-        if (nv == 1) return launch_rows(warp_kernel<1>, grid, 32 * kWarpRows, a, stream);
-        if (nv == 2) return launch_rows(warp_kernel<2>, grid, 32 * kWarpRows, a, stream);
-        return launch_rows(warp_kernel<4>, grid, 32 * kWarpRows, a, stream);
-    }
     int sms = 0;
     if (device_sms(&sms) != cudaSuccess) return S12_ERR_CUDA;
-    // few rows: as many threads as vectors, so that each loads once; many
-    // rows: two vectors a thread, so that more rows share an SM
-    const int want = c.rows <= 2 * sms ? 1 : 2;
-    int nv = want;
-    while (nv * kMaxThreads < vecs) nv *= 2;
-    const unsigned threads = static_cast<unsigned>(std::min(kMaxThreads, ((vecs + nv - 1) / nv + 31) / 32 * 32));
-    const unsigned grid = static_cast<unsigned>(c.rows);
-    if (nv == 1) return launch_rows(block_kernel<1>, grid, threads, a, stream);
-    if (nv == 2) return launch_rows(block_kernel<2>, grid, threads, a, stream);
-    return launch_rows(block_kernel<4>, grid, threads, a, stream);
+    return c.normed ? launch_kind<false>(a, sms, stream) : launch_kind<true>(a, sms, stream);
 }
 
 }  // namespace s12

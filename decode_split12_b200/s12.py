@@ -47,6 +47,7 @@ EXPORTED = (
 
 S12_TYPE_BF16 = 0
 S12_TYPE_F32 = 1
+S12_WS_HEAD = 4096
 
 
 class S12Error(RuntimeError):
@@ -466,6 +467,13 @@ def _expect(t: torch.Tensor, shape, dtypes, name: str):
         raise ValueError(f"{name}: expected {tuple(shape)} of {dtypes}, got {tuple(t.shape)} of {t.dtype}")
 
 
+def _workspace(nbytes: int, device) -> torch.Tensor:
+    """nbytes of device memory, zero where a call needs it."""
+    ws = torch.empty(max(nbytes, S12_WS_HEAD), dtype=torch.uint8, device=device or "cuda")
+    ws[:S12_WS_HEAD].zero_()
+    return ws
+
+
 def _or_empty(t: torch.Tensor | None, like: torch.Tensor, shape, dtype, dtypes, name: str) -> torch.Tensor:
     """An output: the tensor that is given, checked, or a new one."""
     if t is None:
@@ -535,9 +543,9 @@ def s12_gemm_i8_ws_bytes(M: int) -> int:
 
 
 def gemm_i8_workspace(M: int, N: int = 0, K: int = 0, device=None) -> torch.Tensor:
-    """A zero-filled workspace for s12_gemm_i8 with M tokens (its size does
-    not depend on N and K)."""
-    return torch.zeros(max(s12_gemm_i8_ws_bytes(M), 256), dtype=torch.uint8, device=device or "cuda")
+    """A workspace for s12_gemm_i8 with M tokens (its size does not depend on
+    N and K)."""
+    return _workspace(s12_gemm_i8_ws_bytes(M), device)
 
 
 def s12_gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -569,10 +577,9 @@ def s12_moe_ws_bytes(gate_up: View, down: View, experts: int, tokens: int, top_k
 
 
 def moe_workspace(gate_up: View, down: View, experts: int, tokens: int, top_k: int, device=None) -> torch.Tensor:
-    """A zero-filled workspace for s12_moe and s12_moe_routed with these
-    containers and top_k, for up to `tokens` tokens."""
-    need = s12_moe_ws_bytes(gate_up, down, experts, tokens, top_k)
-    return torch.zeros(max(need, 256), dtype=torch.uint8, device=device or "cuda")
+    """A workspace for s12_moe and s12_moe_routed with these containers and
+    top_k, for up to `tokens` tokens."""
+    return _workspace(s12_moe_ws_bytes(gate_up, down, experts, tokens, top_k), device)
 
 
 def _moe_io(down: View, x: torch.Tensor, experts: int, y, f32: bool):

@@ -93,6 +93,7 @@ extern "C" {
 #define S12_GEMM_MAX_PROBLEMS 16 /* matrices per s12_gemm_skinny_multi call */
 #define S12_NORM_MAX_COLS 32768  /* longest row of s12_rmsnorm and s12_quant_i8 */
 #define S12_GEMM_I8_MAX_K 131056 /* columns of s12_gemm_i8: its int32 sums are exact */
+#define S12_WS_HEAD 4096         /* zero bytes in front of the workspaces of s12_moe and s12_gemm_i8 */
 #define S12_MOE_MAX_TOKENS 64   /* tokens of one s12_moe call */
 #define S12_MOE_MAX_TOP_K 8     /* experts a token is sent to */
 #define S12_MOE_MAX_EXPERTS 256
@@ -387,9 +388,8 @@ int s12_gemm_skinny_multi(const s12_view *views, int count, const uint16_t *cons
 /* ---- mixture-of-experts layer ---- */
 
 /* Workspace bytes s12_moe and s12_moe_routed need for these containers (0
- * for invalid arguments).  The size grows with each of tokens, top_k and
- * experts, so one sized for the largest call serves smaller ones of the
- * same containers. */
+ * for invalid arguments).  The size grows with tokens and top_k, so one
+ * sized for the largest call serves smaller ones of the same containers. */
 size_t s12_moe_ws_bytes(const s12_view *gate_up, const s12_view *down, int experts, int tokens, int top_k);
 
 /* Follows: [W] "What does 'lossless' mean for LLM weights?" (decode into
@@ -419,10 +419,11 @@ size_t s12_moe_ws_bytes(const s12_view *gate_up, const s12_view *down, int exper
  *   ids, weights: device int32 and FP32, tokens x top_k, or NULL: the chosen
  *            experts, largest score first, and their weights.
  *   ws:      device workspace of s12_moe_ws_bytes bytes (else
- *            S12_ERR_CAPACITY), ZERO-FILLED before its first use.  Calls of
+ *            S12_ERR_CAPACITY), whose first S12_WS_HEAD bytes are ZERO
+ *            before its first use and zero again after every call.  Calls of
  *            any shapes for which it is large enough may use it one after
- *            the other, captured in a graph or not.  Calls that may run at
- *            the same time need different workspaces.
+ *            the other, captured in a graph or not, s12_gemm_i8's too.
+ *            Calls that may run at the same time need different workspaces.
  * The scores are sums in 64 bits.  The products accumulate in FP32 and the
  * hidden values are held as the sum of two BF16 values, so y is within 1e-3
  * of the sum of its terms' magnitudes before its own rounding, as in
@@ -510,9 +511,10 @@ size_t s12_gemm_i8_ws_bytes(int64_t M);
  *   y: device, M x N row-major, y_type S12_TYPE_BF16 (2-byte alignment) or
  *      S12_TYPE_F32 (4-byte), overwritten.
  *   ws: device workspace of s12_gemm_i8_ws_bytes(M) bytes (else
- *      S12_ERR_CAPACITY), ZERO-FILLED before its first use; calls of any
- *      shapes for which it is large enough may use it one after the other.
- *      Calls that may run at the same time need different workspaces.
+ *      S12_ERR_CAPACITY), whose first S12_WS_HEAD bytes are ZERO before its
+ *      first use and zero again after every call.  Calls of any shapes for
+ *      which it is large enough may use it one after the other, s12_moe's
+ *      too.  Calls that may run at the same time need different workspaces.
  * K is a multiple of 16 up to S12_GEMM_I8_MAX_K; 0 <= M, N < 2^31 (M == 0 or
  * N == 0 does nothing); else S12_ERR_SHAPE.  All values of int8 are allowed.
  * The scales multiply the sum in FP32, x_scale first, and y is rounded once;

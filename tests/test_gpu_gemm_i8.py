@@ -50,7 +50,7 @@ def test_shapes(s12, M, N, K):
     assert torch.equal(y32.to(torch.bfloat16), y.view(torch.bfloat16))
     assert int(flag.item()) == 0
     # the counters are zero again
-    assert int(ws[:592].to(torch.int32).sum()) == 0
+    assert int(ws[:s12.S12_WS_HEAD].to(torch.int32).sum()) == 0
 
 
 @pytest.mark.parametrize("K", [131056, 65536])

@@ -116,17 +116,23 @@ def test_moe_small_and_odd_shapes(s12, T, E, k, H, F):
     check(y32, ref, tol, bf16=False)
     assert torch.equal(y32.to(torch.bfloat16), y.view(torch.bfloat16))
     # the words that have to be zero between calls are
-    assert int(ws[:256].to(torch.int32).sum()) == 0
+    assert int(ws[:s12.S12_WS_HEAD].to(torch.int32).sum()) == 0
 
 
 def test_one_workspace_for_calls_of_any_shape(s12):
     """Only the first words have to be zero: layers of other shapes may use the workspace in turn."""
     cases = [(Layer(s12, E, H, F, E), T, k) for T, E, k, H, F in ((64, 4, 2, 384, 256), (1, 8, 2, 256, 640),
                                                                   (9, 40, 3, 128, 128), (33, 2, 1, 512, 128))]
-    need = max(s12.s12_moe_ws_bytes(*L.views, L.E, T, k) for L, T, k in cases)
-    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    need = max([s12.s12_moe_ws_bytes(*L.views, L.E, T, k) for L, T, k in cases] + [s12.s12_gemm_i8_ws_bytes(300)])
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    ws[:s12.S12_WS_HEAD] = 0
+    q = torch.randint(-128, 128, (300, 256), dtype=torch.int8, device="cuda")
+    one = torch.ones(300, device="cuda")
     for _ in range(2):
         for L, T, k in cases:
+            # (the 8-bit product between them, with parts of tiles joined)
+            prod = s12.s12_gemm_i8(q, one, q, one, ws=ws, f32=True)
+            assert torch.equal(prod.double(), q.double() @ q.double().T)
             x = L.tokens(T, k)
             y, ids, w = s12.s12_moe(*L.views, L.E, x, L.router, k, ws=ws)
             check(y, *reference(L, x, *choose(L, x, k, True)))
@@ -234,6 +240,17 @@ def test_one_workspace_for_calls_of_different_tokens(s12):
             want, weights = choose(L, x, 2, True)
             check(y, *reference(L, x, want, weights))
             first[T] = (y, ids, w)
+
+
+def test_workspace_grows_with_tokens(s12):
+    """The size for the most tokens serves every smaller number of them."""
+    for E, H, F in ((8, 512, 384), (64, 256, 128), (2, 384, 1152)):
+        v = []
+        for rows, cols in ((E * 2 * F, H), (E * H, F)):
+            v.append(s12.s12_open(s12.s12_encode(torch.zeros(rows, cols, dtype=torch.int16, device="cuda"))))
+        for k in (1, 2):
+            sizes = [s12.s12_moe_ws_bytes(*v, E, T, k) for T in range(1, 65)]
+            assert sizes == sorted(sizes)
 
 
 def test_nan_token_leaves_the_others(s12):
