@@ -837,12 +837,13 @@ def stack_extras(world, layers: int = 32, steps: int = 10):
     output (BF16) feeds the next layer: per layer q, k, v, o in one grouped
     launch (attention is outside the path: o reads the layer input in its
     place), gate/up with the SwiGLU epilogue, down with a BF16 output, then
-    an RMS normalisation (torch, standing in for the model's norm layers,
-    which are outside the path) so the activations neither vanish nor blow
+    the RMS norm (s12_rmsnorm), so the activations neither vanish nor blow
     up over the layers.
     Plus an 8-expert MoE block (gate, up 14336x4096, down 4096x14336 per
     expert) with top-2 routing of 64 tokens: experts with >= 9 tokens use the
-    skinny GEMM (rows padded to 16), the rest the GEMV."""
+    skinny GEMM (rows padded to 16), the rest the GEMV.  And the same block as
+    whole layers (s12_moe: routing, SwiGLU and weighted sum included) for 1, 8
+    and 64 tokens."""
     import torch
 
     from decode_split12_b200 import s12
@@ -904,8 +905,7 @@ def stack_extras(world, layers: int = 32, steps: int = 10):
                 s12.s12_gemv_multi(lv[:4], [h] * 4, yp, ws=ws)
                 s12.s12_gemv_swiglu(lv[4], h, hid, ws=ws)
                 s12.s12_gemv_bf16(lv[5], hid, yd, ws=ws)
-                hs[l + 1].view(torch.bfloat16).copy_(
-                    torch.nn.functional.rms_norm(yd.view(torch.bfloat16), (Dm,), eps=1e-6))
+                s12.s12_rmsnorm(yd, eps=1e-6, y=hs[l + 1])
 
         g = capture(chain)
         for _ in range(3):
@@ -914,8 +914,8 @@ def stack_extras(world, layers: int = 32, steps: int = 10):
         last = hs[layers].view(torch.bfloat16).float()
         out[f"chain_B{B}"] = {"ms_per_pass": round(t * 1e3, 3), "ms_per_token": round(t * 1e3 / B, 3),
                               "effective_bf16_GBs": round(2 * weights / t / 1e9, 1),
-                              "hbm_frac": round(cbytes / t / 1e9 / hbm, 4), "launches_per_pass": 3 * layers,
-                              "norm": "torch rms_norm after each layer (outside the path), in the timed graph",
+                              "hbm_frac": round(cbytes / t / 1e9 / hbm, 4), "launches_per_pass": 4 * layers,
+                              "norm": "s12_rmsnorm after each layer, in the timed graph",
                               "output_finite": bool(torch.isfinite(last).all()),
                               "output_rms": float(last.pow(2).mean().sqrt())}
         del g
@@ -1006,6 +1006,38 @@ def stack_extras(world, layers: int = 32, steps: int = 10):
         "grouping": "one s12_gemm_skinny_multi over all experts' gate and up, one over all experts' down"}
     del g, experts, calls, stages
     torch.cuda.empty_cache()
+    out["moe_layer_8x_top2"] = moe_layer_extras(world, steps)
+    return out
+
+
+def moe_layer_extras(world, steps: int):
+    """The 8-expert block as whole layers (s12_moe), gate/up and down of all
+    experts stacked in two containers: one launch, for 1, 8 and 64 tokens."""
+    import torch
+
+    from decode_split12_b200 import s12
+    hbm, _, _, _ = load_peaks()
+    E, k = 8, 2
+    F, Dm = wl.MOE_SHAPES["gate"]
+    gen = torch.Generator(device="cuda").manual_seed(2000)
+    gate_up = s12.s12_open(s12.s12_encode(s12.interleave_gate_up(_student_t_gpu(E * F, Dm, gen),
+                                                                 _student_t_gpu(E * F, Dm, gen))))
+    down = s12.s12_open(s12.s12_encode(_student_t_gpu(E * Dm, F, gen)))
+    torch.cuda.empty_cache()
+    router = (torch.randn(E, Dm, generator=gen, device="cuda") / math.sqrt(Dm)).to(torch.bfloat16)
+    ws = s12.moe_workspace(gate_up, down, E, 64, k)
+    out = {}
+    for T in (1, 8, 64):
+        x = dev16(wl.activations(T, Dm, T, 6000))
+        y, ids, weights = s12.s12_moe(gate_up, down, E, x, router, k, ws=ws)
+        met = int(ids.unique().numel())
+        g = capture(lambda: s12.s12_moe(gate_up, down, E, x, router, k, y=y, ids=ids, weights=weights, ws=ws))
+        for _ in range(3):
+            g.replay()
+        t = time_graph(g, steps, world) / steps
+        nbytes = (int(gate_up.container_bytes) + int(down.container_bytes)) * met / E
+        out[f"T{T}"] = {"experts_met": met, "us": round(t * 1e6, 2), "hbm_frac": round(nbytes / t / 1e9 / hbm, 4)}
+        del g
     return out
 
 
