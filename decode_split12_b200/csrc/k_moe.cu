@@ -48,6 +48,7 @@
 #include "s12_device.cuh"
 #include "s12_launch.h"
 #include "s12_stage.cuh"
+#include "s12_tc.cuh"
 
 namespace s12 {
 namespace moe {
@@ -56,20 +57,16 @@ using namespace stage;
 
 constexpr int kWarps = 16;   // warps per CTA of the kernel for few pairs, one CTA per SM
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLargeWarps = 12;  // and of the one for many, beside one that copies x
-constexpr int kLargeThreads = 32 * (kLargeWarps + 1);
 constexpr int kStages = 2;   // stages per warp ring
-constexpr int kAhead = 3;    // units that a CTA of the kernel for many knows in advance
 constexpr int kSegSmall = 8, kSegLarge = 64;  // (token, slot) pairs that share one read of an expert's weights
 constexpr int kMaxSlots = S12_MOE_MAX_TOKENS * S12_MOE_MAX_TOP_K;
 constexpr int kMaxSegs = S12_MOE_MAX_EXPERTS + kMaxSlots / kSegSmall;
 constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
-constexpr uint32_t kLargeRingBytes = kLargeWarps * kStages * kStageBytes;
 
 // A matrix of all experts: expert after expert, rows_e rows each.
 struct __align__(64) Mat {
-    CUtensorMap tm_raw;   // u8 {128, T, R} (strides 128, K), box {128, 2, 16}, 128-byte swizzle
-    CUtensorMap tm_code;  // u8 {64, T, R} (strides 64, K/2), box {64, 2, 16}, 64-byte swizzle
+    CUtensorMap tm_raw;   // u8 {128, T, R} (strides 128, K), box {128, 2, 16} or {128, 1, 128}, 128-byte swizzle
+    CUtensorMap tm_code;  // u8 {64, T, R} (strides 64, K/2), box {64, 2, 16} or {64, 1, 128}, 64-byte swizzle
     const void *meta;     // version 1: base u8[n_tiles]; version 2: (base | count << 8) u16[n_tiles]
     const uint32_t *off;  // version 1: esc_off u32[n_tiles + 1]; version 2: row_esc u32[R + 1]
     const uint16_t *esc;
@@ -97,7 +94,7 @@ struct __align__(64) Params {
     int seg;         // pairs of a segment at most
     int local;       // few pairs: every CTA routes for itself, with x in shared memory
     uint32_t range;  // stages of an item
-    uint32_t pool;   // many pairs: bytes of shared memory for x
+    uint32_t pool;   // many pairs: bytes of shared memory for stages
     // workspace
     uint32_t *sync;         // kSyncWords, zero between calls
     double *scores;         // [tokens][experts]
@@ -119,13 +116,22 @@ struct Shared {
     int ok, last;
 };
 
-// Order of x and h, in 16-byte pieces of 8 values: tile, then 16-column chunk of
-// a lane's 64, then half chunk, then which of n tokens or pairs, then which 64
-// columns of the tile.  A warp's load of one half chunk is then contiguous over
-// them.  h (and x, where many pairs share an expert) comes segment by segment.
-// Inside a piece the values come as 0 4 1 5 2 6 3 7.
+// Order of x and h, in 16-byte pieces of 8 values, which come as 0 4 1 5 2 6 3 7.
+// Few pairs: tile, then 16-column chunk of a lane's 64, then half chunk, then
+// which of n tokens or pairs, then which 64 columns of the tile.  A warp's load
+// of one half chunk is then contiguous over them.  Many: tile, then which 64
+// columns, then which of n pairs, then the piece of the 64 columns, with the 128-byte
+// swizzle.  h (and x, where many pairs share an expert) comes segment by segment.
 __device__ __forceinline__ size_t piece_at(int tile, int chunk, int half, int n, int i, int qh) {
     return ((((static_cast<size_t>(tile) * 4 + chunk) * 2 + half) * n + i) * 2 + qh) * 16;
+}
+
+// Piece c8 of a row.
+template <bool LARGE>
+__device__ __forceinline__ size_t piece_of(int c8, int n, int i) {
+    const int in = c8 & 15;  // of the tile: 64 columns, chunk, half
+    if (LARGE) return (static_cast<size_t>(c8 >> 3) * n + i) * 128 + (((c8 & 7) ^ (i & 7)) << 4);
+    return piece_at(c8 >> 4, (in >> 1) & 3, in & 1, n, i, in >> 3);
 }
 
 // ---------------------------------------------------------------------------
@@ -172,11 +178,10 @@ __device__ __forceinline__ bool grid_meet(const Params &p, Shared *sm, int word)
 // Step 0: x in the products' order, scores, experts.
 
 // Piece c8 of token t, to place i of n.
+template <bool LARGE>
 __device__ __forceinline__ void pack_piece(const Params &p, uint8_t *to, int t, int c8, int n, int i) {
     const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(t) * p.H) + c8);
-    const int in = c8 & 15;  // piece of the tile: 64 columns, chunk, half
-    uint4 *dst = reinterpret_cast<uint4 *>(to + piece_at(c8 >> 4, (in >> 1) & 3, in & 1, n, i, in >> 3));
-    *dst = make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u),
+    *reinterpret_cast<uint4 *>(to + piece_of<LARGE>(c8, n, i)) = make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u),
                       prmt(v.y, v.w, 0x7632u));
 }
 
@@ -186,7 +191,7 @@ __device__ __forceinline__ void pack_x(const Params &p, uint8_t *to, int i0, int
     const int n = p.tokens * per_row;
     for (int i = i0; i < n; i += step) {
         const int t = i / per_row, c8 = i - t * per_row;  // piece c8 of token t
-        pack_piece(p, to, t, c8, p.tokens, t);
+        pack_piece<false>(p, to, t, c8, p.tokens, t);
     }
 }
 
@@ -195,7 +200,7 @@ __device__ __forceinline__ void pack_sorted(const Params &p, const Shared *sm, i
     const int per_row = p.H / 8;
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < pairs * per_row; i += gridDim.x * blockDim.x) {
         const int at = i / per_row, c8 = i - at * per_row, seg = sm->segment[at], first = sm->seg_first[seg];
-        pack_piece(p, p.xp + static_cast<size_t>(first) * p.H * 2, sm->token[at], c8, sm->seg_n[seg], at - first);
+        pack_piece<true>(p, p.xp + static_cast<size_t>(first) * p.H * 2, sm->token[at], c8, sm->seg_n[seg], at - first);
     }
 }
 
@@ -434,12 +439,8 @@ struct Ring {
     int issued, consumed;
 };
 
-// The end of a CTA: copies that a wait left in flight land, and the last CTA
-// sets the workspace's words back to zero.
-__device__ __forceinline__ void finish(const Params &p, Shared *sm, const Ring &rg) {
-    if ((threadIdx.x & 31) == 0)
-        for (int k = rg.consumed; k < rg.issued; ++k)
-            mbar_wait_s(rg.bars + 8u * (k & 1), static_cast<uint32_t>(k >> 1) & 1u);
+// The end of a CTA: the last one sets the workspace's words back to zero.
+__device__ __forceinline__ void leave(const Params &p, Shared *sm) {
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
@@ -884,6 +885,7 @@ __device__ __forceinline__ int used_pairs(const Shared *sm) {
 }
 
 // h from the sums of step 1: two lanes for a pair's row group (8 f, one piece).
+template <bool LARGE>
 __device__ __forceinline__ void make_hidden(const Params &p, const Shared *sm, uint32_t ranges) {
     const int slots = p.tokens * p.top_k;
     const uint32_t G = static_cast<uint32_t>(p.up.G), n = used_pairs(sm) * G, half = threadIdx.x & 1;
@@ -912,10 +914,9 @@ __device__ __forceinline__ void make_hidden(const Params &p, const Shared *sm, u
                 v[i] = pack_bf16(fabsf(r0) < 3.4e38f ? r0 : 0.f, fabsf(r1) < 3.4e38f ? r1 : 0.f);
             }
         }
-        const int in = static_cast<int>(grp & 15u), seg = sm->segment[pos], first = sm->seg_first[seg];
-        const size_t o = static_cast<size_t>(first) * p.F * 2 + piece_at(static_cast<int>(grp >> 4), (in >> 1) & 3, in & 1,
-                                                                         sm->seg_n[seg], static_cast<int>(pos) - first,
-                                                                         in >> 3);
+        const int seg = sm->segment[pos], first = sm->seg_first[seg];
+        const size_t o = static_cast<size_t>(first) * p.F * 2 +
+                         piece_of<LARGE>(static_cast<int>(grp), sm->seg_n[seg], static_cast<int>(pos) - first);
         *reinterpret_cast<uint4 *>((half ? p.lo : p.hi) + o) = make_uint4(v[0], v[1], v[2], v[3]);
     }
 }
@@ -1009,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_small_kernel(const __grid_con
                 if (d1.live) issue_at<2>(p, rg, d1);
             }
             if (grid_meet(p, &sm->s, kBarSums)) {
-                make_hidden(p, &sm->s, sm->step[0].ranges);
+                make_hidden<false>(p, &sm->s, sm->step[0].ranges);
                 if (grid_meet(p, &sm->s, kBarHidden)) {
                     if (ok) small_step<V, 2>(p, sm, p.hi, rg, f2, d0, d1);
                     if (grid_meet(p, &sm->s, kBarDown)) make_y(p, &sm->s, sm->step[1].ranges);
@@ -1017,294 +1018,481 @@ __global__ void __launch_bounds__(kThreads, 1) moe_small_kernel(const __grid_con
             }
         }
     }
-    finish(p, &sm->s, rg);
+    // copies that a wait left in flight land
+    if (lane == 0)
+        for (int k = rg.consumed; k < rg.issued; ++k)
+            mbar_wait_s(rg.bars + 8u * (k & 1), static_cast<uint32_t>(k >> 1) & 1u);
+    leave(p, &sm->s);
 }
 
 // ---------------------------------------------------------------------------
 // Many pairs an expert: up to 64 share a read of its weights.
 //
-// A unit is twelve row groups of a segment, one to a warp, by a range of
-// columns.  All warps of a CTA go through the same columns, so x is read from
-// shared memory, where a thirteenth warp copies it tile by tile (128 columns of
-// the segment's pairs) into a ring; through L1, with every warp at columns of
-// its own, x cost three times the weights' traffic to L2.  Units come from a
-// counter of the grid as items do above, claimed by the warp that copies x.
+// A unit is a block of 128 rows of a segment's expert by a range of columns:
+// D[row][pair] += W[row][k] * x[pair][k] on the tcgen05 tensor cores, 128 columns
+// (a tile of each row) at a time.  W is the product's left side and is kept in
+// TMEM, where the threads that decode it write it from registers: a thread has
+// one row of the tile, which is one lane of TMEM.  (Through mma.sync, as above,
+// every warp reads all of x from shared memory for 16 rows of weights: 64 tokens
+// of 8 experts of 14336 x 4096 took 815 us.)  x and h are copied to shared
+// memory as the product wants them (128-byte swizzle).
+//
+// Warp 0 claims units and copies weights and x into a ring of stages, a tile
+// each; warp 1 issues the products; sixteen warps decode, four to a tile, each
+// four with a place in TMEM of their own.  The four that had a unit's last tile
+// store its sums, while the other twelve decode the next unit's tiles (there are
+// two places for sums).  Every wait is for something of an earlier tile, or of
+// an earlier part of the same tile, so the tiles' order shows that all end.
+// Units come from a counter of the grid as items do above; the first weights of
+// a step are copied while the grid meets.
 
-constexpr int kEights = 2;  // eights of tokens that are multiplied side by side
-constexpr int kMaxX = 16;   // places of the x ring
-constexpr int kUnits = 32;  // the queue: copying x is at most kMaxX units ahead of a warp
+constexpr int kGroups = 4;       // of four warps that decode a tile
+constexpr int kLargeThreads = 32 * (2 + 4 * kGroups);
+constexpr int kAhead = 3;        // units that a CTA knows in advance
+constexpr int kUnits = 32;       // the queue; no warp is more than 16 tiles behind the copies
+constexpr int kMaxRing = 8;      // stages
+constexpr int kBlockRows = 128;
+constexpr uint32_t kTileRaw = kBlockRows * kTile, kTileBytes = kTileRaw + kTileRaw / 2;
+constexpr uint32_t kSumCols = kSegLarge, kPlaceCols = kTile / 2;  // of TMEM: sums, decoded weights
+constexpr uint32_t kTmemCols = 512;
+static_assert(2 * kSumCols + kGroups * kPlaceCols <= kTmemCols, "two places for sums, one for weights a group");
 
 struct LargeShared {
     Shared s;
     Step step[2];
-    unsigned long long queue[2][kUnits];         // ordinal << 32 | unit
-    unsigned long long full[2][kMaxX], empty[2][kMaxX];  // mbarriers of the x ring, by step
-    uint32_t abort;
+    unsigned long long queue[2][kUnits];  // ordinal << 32 | unit
+    // mbarriers, by step
+    unsigned long long weights[2][kMaxRing], x[2][kMaxRing], empty[2][kMaxRing];  // stages: copied, free
+    unsigned long long decoded[2][kGroups], used[2][kGroups];                     // places of decoded weights
+    unsigned long long sums[2][kGroups], stored[2][2];  // a group's last tile multiplied; places of sums free
+    unsigned long long done[2];                                                   // all products of the step
+    uint32_t tmem, abort;
 };
 
 struct Unit {
     uint32_t seg, range, block;
-    int j, n;  // first tile; stages (0: no more units)
+    int j, n;  // first tile; tiles (0: no more units)
 };
 
-// The CTA's unit `ord` (the queue's answer may have to be waited for, with a limit).
+// The CTA's unit `ord`: 1, or 0 when it is not known yet.
+template <int PH>
+__device__ __forceinline__ bool peek(const Params &p, const LargeShared *sm, uint32_t ord, Unit &u) {
+    const Step &st = sm->step[PH - 1];
+    const unsigned long long e = *const_cast<const volatile unsigned long long *>(&sm->queue[PH - 1][ord % kUnits]);
+    if (e >> 32 != ord) return false;
+    const uint32_t it = static_cast<uint32_t>(e);
+    u = Unit{0u, 0u, 0u, 0, 0};
+    if (it >= st.items) return true;
+    const Item i = item_at<PH>(st, it);
+    const int per = static_cast<int>(st.stages) * kNT;
+    u.seg = i.seg;
+    u.range = i.range;
+    u.block = i.grp;
+    u.j = static_cast<int>(i.range) * per;
+    u.n = min(per, mat<PH>(p).T - u.j);
+    return true;
+}
+
+// The same, waiting for it (with a limit; then there are no more units).
 template <int PH>
 __device__ __forceinline__ Unit unit_at(const Params &p, LargeShared *sm, uint32_t ord) {
-    const Step &st = sm->step[PH - 1];
-    Unit o = {0u, 0u, 0u, 0, 0};
-    const volatile unsigned long long *at = &sm->queue[PH - 1][ord % kUnits];
-    unsigned long long e = *at;
-    if (e >> 32 != ord) {
-        const long long t0 = clock64();
-        while (e >> 32 != ord) {
-            if (*const_cast<volatile uint32_t *>(&sm->abort)) return o;
-            if (clock64() - t0 > kWaitCycles) {
-                sm->abort = 1u;
-                give_up(p);
-                return o;
-            }
-            e = *at;
+    Unit u;
+    if (peek<PH>(p, sm, ord, u)) return u;
+    const long long t0 = clock64();
+    while (!peek<PH>(p, sm, ord, u)) {
+        const bool late = clock64() - t0 > kWaitCycles;
+        if (late) {
+            sm->abort = 1u;
+            give_up(p);
         }
+        if (late || *const_cast<volatile uint32_t *>(&sm->abort)) return Unit{0u, 0u, 0u, 0, 0};
     }
-    const uint32_t it = static_cast<uint32_t>(e);
-    if (it >= st.items) return o;
-    const Item i = item_at<PH>(st, it);
-    o.seg = i.seg;
-    o.range = i.range;
-    o.block = i.grp;
-    o.j = static_cast<int>(i.range * st.stages) * kNT;
-    o.n = static_cast<int>(min(st.stages, mat<PH>(p).S - i.range * st.stages));
-    return o;
+    return u;
 }
 
-// The x ring in a step: places of `bytes` bytes, n of them (even, so that the
-// two tiles of a stage lie 64 bytes apart modulo 128 and their reads share no
-// bank).
-struct XRing {
-    uint32_t base, bytes, n;
-    uint32_t at, parity;  // the next place and its phase
+__device__ __forceinline__ bool lost(const Params &p, LargeShared *sm) {
+    sm->abort = 1u;
+    give_up(p);
+    return false;
+}
 
-    __device__ __forceinline__ void advance() {
-        if (++at == n) {
-            at = 0;
-            parity ^= 1u;
-        }
-    }
+// Bytes of the x of n pairs in a stage (one plane), rows rounded up for the product.
+__device__ __forceinline__ uint32_t product_pairs(uint32_t n) { return (n + 15u) & ~15u; }
+
+struct Stages {
+    uint32_t base, bytes, n;
 };
 
 template <int PH>
-__device__ __forceinline__ XRing x_ring(const Params &p, const LargeShared *sm, uint32_t base) {
-    XRing x;
-    x.base = base;
-    x.bytes = static_cast<uint32_t>(sm->s.most) * 256u * PH + 64u;  // (h: two planes)
-    x.n = min(static_cast<uint32_t>(kMaxX), p.pool / x.bytes) & ~1u;
-    x.at = x.parity = 0;
-    return x;
+__device__ __forceinline__ Stages stages_of(const Params &p, const LargeShared *sm, uint32_t base) {
+    Stages s;
+    s.base = base;
+    s.bytes = kTileBytes + product_pairs(static_cast<uint32_t>(sm->s.most)) * 256u * PH;  // (h: two planes)
+    s.n = min(static_cast<uint32_t>(kMaxRing), p.pool / s.bytes);
+    return s;
 }
 
-// A step by the thread that copies x.
 template <int PH>
-__device__ __forceinline__ void copy_x(const Params &p, LargeShared *sm, uint32_t base) {
-    XRing xr = x_ring<PH>(p, sm, base);
-    const int T = mat<PH>(p).T;
-    const size_t row = static_cast<size_t>(T) * kTile * 2;  // bytes of a pair's row
-    uint32_t issued = 0;
+__device__ __forceinline__ uint32_t row_of(const Params &p, const LargeShared *sm, const Unit &u) {
+    return sm->s.seg_expert[u.seg] * static_cast<uint32_t>(mat<PH>(p).G) * kRowsPerGroup + u.block * kBlockRows;
+}
+
+template <int PH>
+__device__ __forceinline__ void copy_weights(const Params &p, LargeShared *sm, const Stages &rs, uint32_t slot,
+                                             uint32_t row, int j) {
+    const Mat &m = mat<PH>(p);
+    const uint32_t st = rs.base + slot * rs.bytes, bar = smem_addr(&sm->weights[PH - 1][slot]);
+    const uint64_t pol = policy_evict_first();
+    mbar_expect_tx_s(bar, kTileBytes);
+    tma3d(st, &m.tm_raw, 0, j, static_cast<int>(row), bar, pol);
+    tma3d(st + kTileRaw, &m.tm_code, 0, j, static_cast<int>(row), bar, pol);
+}
+
+// What one thread of warp 0 has copied in a step: tiles of weights, of x.
+struct Copied {
+    uint32_t weights, x;
+};
+
+// Weights of the first tiles, as far as the ring goes.
+template <int PH>
+__device__ __forceinline__ Copied copy_first(const Params &p, LargeShared *sm, uint32_t base) {
+    const Stages rs = stages_of<PH>(p, sm, base);
+    Copied c = {0u, 0u};
+    for (uint32_t ord = 0; ord < kAhead; ++ord) {
+        const Unit u = unit_at<PH>(p, sm, ord);
+        if (u.n == 0) break;
+        const uint32_t row = row_of<PH>(p, sm, u);
+        for (int t = 0; t < u.n && c.weights < rs.n; ++t) copy_weights<PH>(p, sm, rs, c.weights++, row, u.j + t);
+    }
+    return c;
+}
+
+template <int PH>
+__device__ __forceinline__ void copy_step(const Params &p, LargeShared *sm, uint32_t base, Copied &c) {
+    const Stages rs = stages_of<PH>(p, sm, base);
+    const size_t line = static_cast<size_t>(mat<PH>(p).T) * kTile * 2;  // bytes of a pair's x
+    uint32_t slot = 0, parity = 1;
     bool ok = true;
     for (uint32_t ord = 0; ok; ++ord) {
         const Unit u = unit_at<PH>(p, sm, ord);
         if (u.n == 0) break;
         const uint32_t claimed = atomicAdd(p.sync + (PH == 1 ? kNext1 : kNext2), 1u) + kAhead * gridDim.x;
-        const uint32_t bytes = static_cast<uint32_t>(sm->s.seg_n[u.seg]) * 256u;
-        const size_t off = sm->s.seg_first[u.seg] * row;
-        for (int t = u.j; ok && t < min(u.j + kNT * u.n, T); ++t) {
-            const uint32_t full = smem_addr(&sm->full[PH - 1][xr.at]), dst = xr.base + xr.at * xr.bytes;
-            ok = mbar_wait_s(smem_addr(&sm->empty[PH - 1][xr.at]), xr.parity ^ 1u);
+        const uint32_t row = row_of<PH>(p, sm, u), n = sm->s.seg_n[u.seg], atom = product_pairs(n) * 128u;
+        const size_t off = sm->s.seg_first[u.seg] * line;
+        for (int t = 0; t < u.n; ++t) {
+            ok = mbar_wait_s(smem_addr(&sm->empty[PH - 1][slot]), parity);
             if (!ok) break;
-            mbar_expect_tx_s(full, PH * bytes);
-            const size_t src = off + static_cast<size_t>(t) * bytes;
+            if (c.x == c.weights) {
+                copy_weights<PH>(p, sm, rs, slot, row, u.j + t);
+                ++c.weights;
+            }
+            const uint32_t bar = smem_addr(&sm->x[PH - 1][slot]), dst = rs.base + slot * rs.bytes + kTileBytes;
+            const size_t src = off + static_cast<size_t>(u.j + t) * n * 256u;
+            mbar_expect_tx_s(bar, PH * n * 256u);
 #pragma unroll
-            for (int plane = 0; plane < PH; ++plane)
+            for (int i = 0; i < 2 * PH; ++i)  // 64 columns of a plane
                 asm volatile(
                     "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                        dst + plane * bytes),
-                    "l"((PH == 1 ? p.xp : plane ? p.lo : p.hi) + src), "r"(bytes), "r"(full)
+                        dst + i * atom),
+                    "l"((PH == 1 ? p.xp : i >= 2 ? p.lo : p.hi) + src + (i & 1) * n * 128u), "r"(n * 128u), "r"(bar)
                     : "memory");
-            xr.advance();
-            ++issued;
+            ++c.x;
+            if (++slot == rs.n) {
+                slot = 0;
+                parity ^= 1u;
+            }
         }
         const uint32_t next = ord + kAhead;
         *const_cast<volatile unsigned long long *>(&sm->queue[PH - 1][next % kUnits]) =
             (static_cast<unsigned long long>(next) << 32) | claimed;
     }
-    if (!ok) {
-        sm->abort = 1u;
-        give_up(p);
-    }
-    // every copy lands before the CTA goes on
-    for (uint32_t i = issued > xr.n ? issued - xr.n : 0; i < issued; ++i)
-        mbar_wait_s(smem_addr(&sm->full[PH - 1][i % xr.n]), (i / xr.n) & 1u);
+    // the stages are another step's next
+    for (uint32_t i = c.x > rs.n ? c.x - rs.n : 0; ok && i < c.x; ++i)
+        ok = mbar_wait_s(smem_addr(&sm->empty[PH - 1][i % rs.n]), (i / rs.n) & 1u);
+    if (!ok) lost(p, sm);
 }
 
-__device__ __forceinline__ void arrive_s(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// A warp's way through the weights of a step: its next stage, unit after unit.
-// A unit that has no row group for the warp has stages that are not live: a
-// warp that looked past them for its next row group would wait for units that
-// are claimed only when it has let go of the x of this one.
+// Every copy of a step lands (after a wait that gave up; else they have).
 template <int PH>
-struct LargeFeed {
-    Unit u;
-    uint32_t ord;
-    int k;
+__device__ __forceinline__ void land(const Params &p, LargeShared *sm, const Copied &c) {
+    const uint32_t n = stages_of<PH>(p, sm, 0u).n;
+    for (uint32_t i = c.weights > n ? c.weights - n : 0; i < c.weights; ++i)
+        mbar_wait_s(smem_addr(&sm->weights[PH - 1][i % n]), (i / n) & 1u);
+    for (uint32_t i = c.x > n ? c.x - n : 0; i < c.x; ++i)
+        mbar_wait_s(smem_addr(&sm->x[PH - 1][i % n]), (i / n) & 1u);
+}
 
-    __device__ __forceinline__ void start(const Params &p, LargeShared *sm) {
-        ord = 0;
-        k = 0;
-        u = unit_at<PH>(p, sm, 0);
-    }
+// D[tmem] (+)= A[tmem] * B[smem] for one 128 x N x 16 step, BF16 -> FP32.
+__device__ __forceinline__ void umma_weights(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 
-    __device__ __forceinline__ Desc next(const Params &p, LargeShared *sm) {
-        const Mat &m = mat<PH>(p);
-        Desc d;
-        d.live = d.last = false;
-        d.it = d.row16 = 0;
-        d.j = 0;
-        if (u.n && k == u.n) {
-            k = 0;
-            u = unit_at<PH>(p, sm, ++ord);
-        }
-        if (u.n) {
-            const uint32_t grp = u.block * kLargeWarps + (threadIdx.x >> 5);
-            d.row16 = sm->s.seg_expert[u.seg] * static_cast<uint32_t>(m.G) + grp;
-            d.j = u.j + kNT * k;
-            d.live = grp < static_cast<uint32_t>(m.G);
-            ++k;
-        }
-        return d;
-    }
-};
+// BF16 x BF16 -> FP32, both operands K-major, M = 128, N = n.
+__device__ __forceinline__ uint32_t product_desc(uint32_t n) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((kBlockRows >> 4) << 24);
+}
 
-// A step by one of the warps that multiply.  d0 and d1 are its first stages,
-// whose copies are in flight.  False when a wait gave up.
-template <int V, int PH, int NT>
-__device__ __forceinline__ bool large_step(const Params &p, LargeShared *sm, uint32_t xbase, Ring &rg,
-                                           LargeFeed<PH> &feed, Desc d0, Desc d1) {
-    const Mat &m = mat<PH>(p);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, tq = q >> 1, qh = q & 1;
-    const int slots = p.tokens * p.top_k;
-    const size_t rows = static_cast<size_t>(m.G) * kRowsPerGroup;  // of an expert
-    XRing xr = x_ring<PH>(p, sm, xbase);
-    Words w0 = load_words<V>(m, d0);
-    read_ahead<V>(m, w0);
-    for (uint32_t ord = 0;; ++ord) {
+// A step by the thread that issues the products.
+template <int PH>
+__device__ __forceinline__ void multiply_step(const Params &p, LargeShared *sm, uint32_t base, uint32_t tmem) {
+    const Stages rs = stages_of<PH>(p, sm, base);
+    uint32_t slot = 0, parity = 0, group = 0, gparity = 0;
+    bool ok = true;
+    for (uint32_t ord = 0; ok; ++ord) {
         const Unit u = unit_at<PH>(p, sm, ord);
         if (u.n == 0) break;
-        const uint32_t grp = u.block * kLargeWarps + warp;
-        const bool mine = grp < static_cast<uint32_t>(m.G);  // (the last unit of a segment may have fewer groups)
-        const int pairs = sm->s.seg_n[u.seg], first = sm->s.seg_first[u.seg], nts = (pairs + 7) >> 3;
-        const uint32_t half = static_cast<uint32_t>(pairs) * 32u;
-        // (columns past the last pair repeat it; their results are dropped)
-        const uint32_t off = static_cast<uint32_t>(g) * 32u + qh * 16u;
-        const uint32_t off_last = static_cast<uint32_t>(min(8 * (nts - 1) + g, pairs - 1)) * 32u + qh * 16u;
-        float acc[NT][4];
+        const uint32_t n = product_pairs(sm->s.seg_n[u.seg]), idesc = product_desc(n), atom = n * 128u;
+        const uint32_t sums = tmem + (ord & 1u) * kSumCols;
+        ok = mbar_wait_s(smem_addr(&sm->stored[PH - 1][ord & 1u]), ((ord >> 1) & 1u) ^ 1u);
+        for (int t = 0; ok && t < u.n; ++t) {
+            ok = mbar_wait_s(smem_addr(&sm->x[PH - 1][slot]), parity) &&
+                 mbar_wait_s(smem_addr(&sm->decoded[PH - 1][group]), gparity);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t xa = rs.base + slot * rs.bytes + kTileBytes;
+            const uint32_t wa = tmem + 2u * kSumCols + group * kPlaceCols;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int k = 0; k < kTile / 16; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-#pragma unroll 1
-        for (int k = 0; k < u.n; ++k) {
-            const bool two = u.j + kNT * k + 1 < m.T;
-            XRing x1 = xr;
-            x1.advance();
-            const uint32_t slot = static_cast<uint32_t>(rg.consumed & 1);
-            bool ok = mbar_wait_s(smem_addr(&sm->full[PH - 1][xr.at]), xr.parity);
-            if (ok && two) ok = mbar_wait_s(smem_addr(&sm->full[PH - 1][x1.at]), x1.parity);
-            if (ok && mine) ok = mbar_wait_s(rg.bars + 8u * slot, static_cast<uint32_t>(rg.consumed >> 1) & 1u);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
-                if (lane == 0) give_up(p);
-                sm->abort = 1u;
-                return false;
+                for (int plane = 0; plane < PH; ++plane)
+                    umma_weights(sums, wa + k * 8,
+                                 tc::smem_desc_sw128(xa + (2 * plane + (k >> 2)) * atom + (k & 3) * 32u), idesc,
+                                 t == 0 && k == 0 && plane == 0 ? 0u : 1u);
+            tc::umma_commit(smem_addr(&sm->used[PH - 1][group]));
+            tc::umma_commit(smem_addr(&sm->empty[PH - 1][slot]));
+            if (t + 1 == u.n) tc::umma_commit(smem_addr(&sm->sums[PH - 1][group]));
+            if (++slot == rs.n) {
+                slot = 0;
+                parity ^= 1u;
             }
-            Words w1 = load_words<V>(m, d1);
-            Desc d2;
-            if (mine) {
-                const bool live = two || tq == 0;  // the lane's tile exists (else zeros from the copy)
-                const uint32_t xl = xr.base + (tq ? x1.at : xr.at) * xr.bytes;
-                auto multiply = [&](int c, const uint32_t (&wa)[8], const uint32_t (&wb)[8]) {
-                    const uint32_t xc = xl + 2u * c * half;
-#pragma unroll
-                    for (int n0 = 0; n0 < NT; n0 += kEights)
-                        if (n0 < nts) {
-#pragma unroll
-                            for (int plane = 0; plane < PH; ++plane) {
-                                uint32_t xw[kEights][8];
-#pragma unroll
-                                for (int n = 0; n < kEights; ++n) {
-                                    // (eights past the last repeat it; their sums are dropped)
-                                    const uint32_t at = xc + plane * 8u * half +
-                                                        (n0 + n + 1 >= nts ? off_last : off + 256u * (n0 + n));
-                                    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-                                    if (live) {
-                                        a = lds128(at);
-                                        b = lds128(at + half);
-                                    }
-                                    xw[n][0] = a.x; xw[n][1] = a.y; xw[n][2] = a.z; xw[n][3] = a.w;
-                                    xw[n][4] = b.x; xw[n][5] = b.y; xw[n][6] = b.z; xw[n][7] = b.w;
-                                }
-                                chunk_mma(acc, n0, wa, wb, xw);
-                            }
-                        }
-                };
-                auto refill = [&]() {
-                    // the stage is in registers: hand it back to the copy
-                    // engine.  (It was read only, which needs no proxy fence.)
-                    __syncwarp();
-                    d2 = feed.next(p, sm);
-                    if (d2.live) issue_at<PH>(p, rg, d2);
-                    read_ahead<V>(m, w1);
-                };
-                stage_products<V>(p, m, d0, w0, rg.base + slot * kStageBytes, multiply, refill);
-                ++rg.consumed;
-            } else {
-                d2 = feed.next(p, sm);
-                if (d2.live) issue_at<PH>(p, rg, d2);
-                read_ahead<V>(m, w1);
+            if (++group == kGroups) {
+                group = 0;
+                gparity ^= 1u;
             }
-            d0 = d1;
-            d1 = d2;
-            w0 = w1;
-            __syncwarp();
-            if (lane == 0) {
-                arrive_s(smem_addr(&sm->empty[PH - 1][xr.at]));
-                if (two) arrive_s(smem_addr(&sm->empty[PH - 1][x1.at]));
-            }
-            xr.advance();
-            if (two) xr.advance();
         }
-        if (!mine) continue;
-        // lane (g, q) holds rows g and g + 8 of pairs 2q and 2q + 1 of each eight
-        float *to = (PH == 1 ? p.gu : p.d) + (static_cast<size_t>(u.range) * slots + first + 2 * q) * rows +
-                    static_cast<size_t>(grp) * kRowsPerGroup + g;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (8 * nt + 2 * q + e < pairs) {
-                    __stcg(to + (8 * nt + e) * rows, acc[nt][e]);
-                    __stcg(to + (8 * nt + e) * rows + 8, acc[nt][2 + e]);
-                }
     }
+    if (!ok) lost(p, sm);
+    // every product is over before its memory serves something else
+    tc::umma_commit(smem_addr(&sm->done[PH - 1]));
+    mbar_wait_s(smem_addr(&sm->done[PH - 1]), 0);
+}
+
+// A group's way through a step: every fourth tile, across units.
+struct Way {
+    uint32_t ord, row;
+    int j, k, n;  // the unit's first tile, the tile in it, its tiles (0: the end)
+};
+
+template <int PH>
+__device__ __forceinline__ void enter(const Params &p, const LargeShared *sm, Way &w, const Unit &u) {
+    w.n = u.n;
+    w.j = u.j;
+    if (u.n) w.row = row_of<PH>(p, sm, u);
+}
+
+// The way `tiles` on; false (and w as it was) when a unit is not known yet.
+template <int PH, bool WAIT>
+__device__ __forceinline__ bool go(const Params &p, LargeShared *sm, Way &w, int tiles) {
+    Way to = w;
+    to.k += tiles;
+    while (to.n && to.k >= to.n) {
+        to.k -= to.n;
+        ++to.ord;
+        Unit u;
+        if (WAIT)
+            u = unit_at<PH>(p, sm, to.ord);
+        else if (!peek<PH>(p, sm, to.ord, u))
+            return false;
+        enter<PH>(p, sm, to, u);
+    }
+    w = to;
     return true;
 }
 
+// Metadata of the thread's tile row, as loaded words.
+struct RowWords {
+    uint32_t w0, w1, w2, w3;  // version 1: base, esc_off[t], esc_off[t + 1], its first escape (later);
+                              // version 2: tmeta[t], and of the three tiles before that are in the unit
+};
+
 template <int V, int PH>
-__device__ __forceinline__ bool large_step(const Params &p, LargeShared *sm, uint32_t xbase, Ring &rg,
-                                           LargeFeed<PH> &feed, const Desc &d0, const Desc &d1) {
-    if (sm->s.most <= 16) return large_step<V, PH, 2>(p, sm, xbase, rg, feed, d0, d1);
-    if (sm->s.most <= 32) return large_step<V, PH, 4>(p, sm, xbase, rg, feed, d0, d1);
-    return large_step<V, PH, 8>(p, sm, xbase, rg, feed, d0, d1);
+__device__ __forceinline__ RowWords load_row(const Params &p, const Way &w, int r) {
+    const Mat &m = mat<PH>(p);
+    RowWords o = {0u, 0u, 0u, 0u};
+    if (w.n == 0) return o;
+    const size_t at = static_cast<size_t>(w.row + r) * m.T + w.j + w.k;
+    if (V == 1) {
+        o.w0 = __ldg(static_cast<const uint8_t *>(m.meta) + at);
+        o.w1 = __ldg(m.off + at);
+        o.w2 = __ldg(m.off + at + 1);
+    } else {
+        const uint16_t *tm = static_cast<const uint16_t *>(m.meta) + at;
+        o.w0 = __ldg(tm);
+        if (w.k >= 1) o.w1 = __ldg(tm - 1);
+        if (w.k >= 2) o.w2 = __ldg(tm - 2);
+        if (w.k >= 3) o.w3 = __ldg(tm - 3);
+    }
+    return o;
+}
+
+template <int V>
+__device__ __forceinline__ void first_escape(const Mat &m, RowWords &w) {
+    if (V == 1 && w.w1 != w.w2 && w.w1 < m.n_esc) w.w3 = __ldg(m.esc + w.w1);
+}
+
+// Version 2: escapes of a row before tile j.
+__device__ __forceinline__ uint32_t escapes_before(const Mat &m, size_t row, int j) {
+    const uint16_t *tm = static_cast<const uint16_t *>(m.meta) + row * m.T;
+    uint32_t n = __ldg(m.off + row);
+#pragma unroll 16
+    for (int t = 0; t < j; ++t) n += __ldg(tm + t) >> 8;
+    return n;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// The thread's row (r of the block) of a tile: its 128 weights to its lane of TMEM.
+template <int V>
+__device__ __forceinline__ void decode_row(const Params &p, const Mat &m, uint32_t st, uint32_t to, int r, uint32_t base,
+                                           uint32_t from, uint32_t end, uint32_t ev) {
+    if (p.err && base > static_cast<uint32_t>(kMaxBase)) raise_flag(p.err, S12_FLAG_BASE);
+    const uint32_t raw = st + static_cast<uint32_t>(r) * 128u, rsw = static_cast<uint32_t>(r) & 7u;
+    const uint32_t code = st + kTileRaw + static_cast<uint32_t>(r) * 64u, csw = (static_cast<uint32_t>(r) >> 1) & 3u;
+    const uint32_t B2 = base * 0x00800080u, limit = from <= end ? min(end, m.n_esc) : 0u;
+    const uint32_t known = V == 1 ? from : ~0u;
+    uint32_t idx = from;
+#pragma unroll 1
+    for (uint32_t c = 0; c < 4; ++c) {  // 32 columns
+        const uint4 k = lds128(code + ((c ^ csw) << 4));
+        const uint4 a = lds128(raw + (((2u * c) ^ rsw) << 4)), b = lds128(raw + (((2u * c + 1u) ^ rsw) << 4));
+        uint32_t w[2][8];
+        decode_pairs(a.x, a.y, k.x, B2, w[0]);
+        decode_pairs(a.z, a.w, k.y, B2, w[0] + 4);
+        decode_pairs(b.x, b.y, k.z, B2, w[1]);
+        decode_pairs(b.z, b.w, k.w, B2, w[1] + 4);
+        if (from != end) {
+            const uint32_t n0 = __popc(escape_nibbles(k.x)) + __popc(escape_nibbles(k.y));
+            const uint32_t n1 = __popc(escape_nibbles(k.z)) + __popc(escape_nibbles(k.w));
+            if (n0) patch(w[0], make_uint2(k.x, k.y), idx, limit, known, ev, m.esc, p.err);
+            idx += n0;
+            if (n1) patch(w[1], make_uint2(k.z, k.w), idx, limit, known, ev, m.esc, p.err);
+            idx += n1;
+        }
+        __syncwarp();
+        uint32_t v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = w[i >> 3][i & 7];
+        tmem_st16(to + c * 16u, v);
+    }
+    if (idx != end && p.err) raise_flag(p.err, S12_FLAG_ESC_COUNT);
+}
+
+// A step by one of the warps that decode.
+template <int V, int PH>
+__device__ __forceinline__ void decode_step(const Params &p, LargeShared *sm, uint32_t base, uint32_t tmem) {
+    const Mat &m = mat<PH>(p);
+    const Stages rs = stages_of<PH>(p, sm, base);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = (warp - 2) >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;  // TMEM lanes 32 quad on are this warp's
+    const uint32_t place = tmem + lanes + 2u * kSumCols + static_cast<uint32_t>(group) * kPlaceCols;
+    uint32_t slot = static_cast<uint32_t>(group), parity = 0, gparity = 0, sparity = 0, run = 0;
+    Way at = {0u, 0u, 0, 0, 0}, next;
+    enter<PH>(p, sm, at, unit_at<PH>(p, sm, 0));
+    go<PH, true>(p, sm, at, group);
+    RowWords w0 = load_row<V, PH>(p, at, r), w1 = {0u, 0u, 0u, 0u}, w2 = w1;
+    first_escape<V>(m, w0);
+    next = at;
+    bool known = false;  // `next` is the tile after this one, and w1 its words
+    while (at.n) {
+        while (slot >= rs.n) {
+            slot -= rs.n;
+            parity ^= 1u;
+        }
+        // two tiles ahead: a tile's words, one ahead: the escape they point to
+        if (!known && (known = go<PH, false>(p, sm, next, kGroups))) w1 = load_row<V, PH>(p, next, r);
+        Way after = next;
+        const bool known2 = known && go<PH, false>(p, sm, after, kGroups);
+        if (known2) w2 = load_row<V, PH>(p, after, r);
+        if (known) first_escape<V>(m, w1);
+
+        const bool ok = mbar_wait_s(smem_addr(&sm->weights[PH - 1][slot]), parity) &&
+                        mbar_wait_s(smem_addr(&sm->used[PH - 1][group]), gparity ^ 1u);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+            lost(p, sm);
+            return;
+        }
+        tc::tc_fence_after();
+        uint32_t from = w0.w1, end = w0.w2;
+        if (V == 2) {
+            if (at.k < kGroups) run = escapes_before(m, at.row + r, at.j);
+            from = run + (w0.w1 >> 8) + (w0.w2 >> 8) + (w0.w3 >> 8);
+            run = end = from + (w0.w0 >> 8);
+        }
+        decode_row<V>(p, m, rs.base + slot * rs.bytes, place, r, V == 1 ? w0.w0 : w0.w0 & 0xFFu, from, end, w0.w3);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            tc::bar_arrive(smem_addr(&sm->decoded[PH - 1][group]));
+            tc::bar_arrive(smem_addr(&sm->empty[PH - 1][slot]));
+        }
+        gparity ^= 1u;
+        slot += kGroups;
+        if (at.k + 1 == at.n) {
+            // the unit's sums, a lane of TMEM for each row
+            const Unit u = unit_at<PH>(p, sm, at.ord);
+            const int pairs = sm->s.seg_n[u.seg];
+            const size_t rows = static_cast<size_t>(m.G) * kRowsPerGroup;  // of an expert
+            const uint32_t d = at.ord & 1u, from_sums = tmem + lanes + d * kSumCols;
+            float *to = (PH == 1 ? p.gu : p.d) +
+                        (static_cast<size_t>(u.range) * (p.tokens * p.top_k) + sm->s.seg_first[u.seg]) * rows +
+                        static_cast<size_t>(u.block) * kBlockRows + r;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_s(smem_addr(&sm->sums[PH - 1][group]), sparity))) {
+                lost(p, sm);
+                return;
+            }
+            sparity ^= 1u;
+            tc::tc_fence_after();
+            for (int c = 0; c < pairs; c += 16) {
+                uint32_t v[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tc::tmem_ld4(from_sums + c + 4 * i, v[i]);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < pairs) __stcg(to + (c + i) * rows, __uint_as_float(v[i >> 2][i & 3]));
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(smem_addr(&sm->stored[PH - 1][d]));
+        }
+        if (known) {
+            at = next;
+            w0 = w1;
+            next = after;
+            w1 = w2;
+            known = known2;
+        } else {
+            go<PH, true>(p, sm, at, kGroups);
+            w0 = load_row<V, PH>(p, at, r);
+            first_escape<V>(m, w0);
+            next = at;
+        }
+    }
 }
 
 // The x that this thread wrote goes to copies (by other SMs, after the grid met).
@@ -1314,28 +1502,39 @@ template <int V>
 __global__ void __launch_bounds__(kLargeThreads, 1) moe_large_kernel(const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    LargeShared *sm = reinterpret_cast<LargeShared *>(base + kLargeRingBytes);
-    const uint32_t xbase = smem_addr(base) + kLargeRingBytes + ((sizeof(LargeShared) + 127) & ~size_t(127));
+    LargeShared *sm = reinterpret_cast<LargeShared *>(base);
+    const uint32_t stages = smem_addr(base) + ((sizeof(LargeShared) + 1023) & ~size_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool copies_x = warp == kLargeWarps;
-    Ring rg;
-    rg.bars = smem_addr(sm->s.bars) + static_cast<uint32_t>(warp) * kStages * 8u;
-    rg.base = smem_addr(base) + static_cast<uint32_t>(warp) * kStages * kStageBytes;
-    rg.issued = rg.consumed = 0;
-    if (lane == 0) {
-        if (copies_x) {
-            for (int i = 0; i < 2 * kMaxX; ++i) {
-                mbar_init_s(smem_addr(&sm->full[0][0] + i), 1);
-                mbar_init_s(smem_addr(&sm->empty[0][0] + i), kLargeWarps);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            for (int s = 0; s < kMaxRing; ++s) {
+                mbar_init_s(smem_addr(&sm->weights[i][s]), 1);
+                mbar_init_s(smem_addr(&sm->x[i][s]), 1);
+                mbar_init_s(smem_addr(&sm->empty[i][s]), 4 + 1);  // the warps that decode it, the products
             }
-        } else {
-            for (int s = 0; s < kStages; ++s) mbar_init_s(rg.bars + 8u * s, 1);
+            for (int g = 0; g < kGroups; ++g) {
+                mbar_init_s(smem_addr(&sm->decoded[i][g]), 4);
+                mbar_init_s(smem_addr(&sm->used[i][g]), 1);
+                mbar_init_s(smem_addr(&sm->sums[i][g]), 1);
+            }
+            for (int d = 0; d < 2; ++d) mbar_init_s(smem_addr(&sm->stored[i][d]), 4);
+            mbar_init_s(smem_addr(&sm->done[i]), 1);
         }
+        sm->abort = 0u;
         fence_barrier_init();
     }
+    if (warp == 1) {
+        tc::tmem_alloc(smem_addr(&sm->tmem), kTmemCols);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = sm->tmem;
     bool ok = true;
     if (!p.ids_in) {
-        const int warps = kLargeWarps + 1, u0 = warp * gridDim.x + blockIdx.x, step = gridDim.x * warps;
+        constexpr int kWarpsHere = kLargeThreads / 32;
+        const int u0 = warp * gridDim.x + blockIdx.x, step = gridDim.x * kWarpsHere;
         if (p.tokens * p.experts >= 1024)
             score<4, 4>(p, p.scores, u0, step);
         else
@@ -1349,57 +1548,66 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_large_kernel(const __gri
             const size_t n = static_cast<size_t>(p.tokens) * p.H;
             for (size_t i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) put_y(p, i, 0.f);
         } else {
-            if (threadIdx.x == 0) sm->step[0] = plan_step<1>(p, &sm->s, kLargeWarps);
-            if (threadIdx.x == 32) sm->step[1] = plan_step<2>(p, &sm->s, kLargeWarps);
+            constexpr int kGroupsOfBlock = kBlockRows / kRowsPerGroup;
+            if (threadIdx.x == 0) sm->step[0] = plan_step<1>(p, &sm->s, kGroupsOfBlock);
+            if (threadIdx.x == 32) sm->step[1] = plan_step<2>(p, &sm->s, kGroupsOfBlock);
             if (threadIdx.x >= 64 && threadIdx.x < 64 + 2 * kUnits) {
                 const uint32_t k = threadIdx.x % kUnits;
                 sm->queue[(threadIdx.x - 64) / kUnits][k] =
                     k < kAhead ? (static_cast<unsigned long long>(k) << 32) | (blockIdx.x + k * gridDim.x) : ~0ull;
             }
-            if (threadIdx.x == 128) sm->abort = 0u;
             pack_sorted(p, &sm->s, used_pairs(&sm->s));
             fence_for_copies();
             __syncthreads();
-            LargeFeed<1> f1;
-            LargeFeed<2> f2;
-            Desc d0, d1;
-            auto begin = [&](auto &f, auto ph) {
-                constexpr int PH = decltype(ph)::value;
-                f.start(p, sm);
-                d0 = f.next(p, sm);
-                if (d0.live) issue_at<PH>(p, rg, d0);
-                d1 = f.next(p, sm);
-                if (d1.live) issue_at<PH>(p, rg, d1);
-            };
+            Copied c1 = {0u, 0u}, c2 = {0u, 0u};
+            const bool copies = warp == 0 && lane == 0, multiplies = warp == 1 && lane == 0;
             // the first weights are copied while the grid meets
-            if (!copies_x) begin(f1, std::integral_constant<int, 1>());
+            if (copies) c1 = copy_first<1>(p, sm, stages);
+            __syncwarp();
             if (grid_meet(p, &sm->s, kBarPack)) {
                 fence_for_copies();
-                if (copies_x) {
-                    if (lane == 0) copy_x<1>(p, sm, xbase);
-                    __syncwarp();
-                } else {
-                    ok = large_step<V, 1>(p, sm, xbase, rg, f1, d0, d1);
-                    if (ok) begin(f2, std::integral_constant<int, 2>());
+                if (copies) {
+                    copy_step<1>(p, sm, stages, c1);
+                    if (!*const_cast<volatile uint32_t *>(&sm->abort)) c2 = copy_first<2>(p, sm, stages);
+                } else if (multiplies) {
+                    multiply_step<1>(p, sm, stages, tmem);
+                } else if (warp >= 2) {
+                    decode_step<V, 1>(p, sm, stages, tmem);
                 }
+                __syncwarp();
                 if (grid_meet(p, &sm->s, kBarSums)) {
-                    make_hidden(p, &sm->s, sm->step[0].ranges);
+                    make_hidden<true>(p, &sm->s, sm->step[0].ranges);
                     fence_for_copies();
                     if (grid_meet(p, &sm->s, kBarHidden)) {
                         fence_for_copies();
-                        if (copies_x) {
-                            if (lane == 0) copy_x<2>(p, sm, xbase);
-                            __syncwarp();
-                        } else if (ok) {
-                            large_step<V, 2>(p, sm, xbase, rg, f2, d0, d1);
+                        const bool on = *const_cast<volatile uint32_t *>(&sm->abort) == 0u;
+                        __syncthreads();
+                        if (on) {
+                            if (copies) {
+                                copy_step<2>(p, sm, stages, c2);
+                            } else if (multiplies) {
+                                multiply_step<2>(p, sm, stages, tmem);
+                            } else if (warp >= 2) {
+                                decode_step<V, 2>(p, sm, stages, tmem);
+                            }
                         }
+                        __syncwarp();
                         if (grid_meet(p, &sm->s, kBarDown)) make_y(p, &sm->s, sm->step[1].ranges);
                     }
                 }
             }
+            if (copies) {
+                land<1>(p, sm, c1);
+                land<2>(p, sm, c2);
+            }
+            __syncwarp();
         }
     }
-    finish(p, &sm->s, rg);
+    leave(p, &sm->s);
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, kTmemCols);
+    }
 }
 
 }  // namespace moe
@@ -1441,12 +1649,11 @@ MoePlan plan(const MoeCall &c) {
                    (c.ids_in || static_cast<uint64_t>(c.tokens) * c.experts * H <= (1u << 18));
         pl.smem = fixed + static_cast<uint32_t>(pl.local ? x_bytes : 0);
     } else {
-        const uint32_t fixed = 1024 + moe::kLargeRingBytes + align_up(sizeof(moe::LargeShared), 128);
+        const uint32_t fixed = 1024 + align_up(sizeof(moe::LargeShared), 1024);
         pl.pool = kSmemLimit - fixed;
         pl.smem = kSmemLimit;
-        static_assert(kSmemLimit - 1024 - moe::kLargeRingBytes - sizeof(moe::LargeShared) - 128 >=
-                          2 * (2 * 256 * moe::kSegLarge + 64),
-                      "x of a stage fits beside the rings");
+        static_assert(kSmemLimit - 2048 - sizeof(moe::LargeShared) >= 3 * (moe::kTileBytes + 2 * 256 * moe::kSegLarge),
+                      "three stages at least");
     }
     // (by the shorter ranges always: a call of fewer tokens never needs more)
     const auto ranges = [](uint64_t cols) {
@@ -1470,10 +1677,10 @@ MoePlan plan(const MoeCall &c) {
     return pl;
 }
 
-int fill_mat(moe::Mat &m, const s12_view *v, int rows_e) {
+int fill_mat(moe::Mat &m, const s12_view *v, int rows_e, int box_tiles, int box_rows) {
     const uint64_t R = v->rows, K = v->cols, T = K / kTile;
-    if (make_tmap_u8_3d(&m.tm_raw, v->raw, 128, T, R, 128, K, 128, stage::kNT, stage::kRowsPerGroup, 128) != S12_OK ||
-        make_tmap_u8_3d(&m.tm_code, v->code, 64, T, R, 64, K / 2, 64, stage::kNT, stage::kRowsPerGroup, 64) != S12_OK)
+    if (make_tmap_u8_3d(&m.tm_raw, v->raw, 128, T, R, 128, K, 128, box_tiles, box_rows, 128) != S12_OK ||
+        make_tmap_u8_3d(&m.tm_code, v->code, 64, T, R, 64, K / 2, 64, box_tiles, box_rows, 64) != S12_OK)
         return S12_ERR_CUDA;
     m.meta = v->version == 1 ? static_cast<const void *>(v->base) : static_cast<const void *>(v->tmeta);
     m.off = v->version == 1 ? v->esc_off : v->row_esc;
@@ -1498,8 +1705,9 @@ int launch_moe(const MoeCall &c, void *ws, size_t ws_bytes, cudaStream_t stream)
     moe::Params p = {};
     p.H = static_cast<int>(c.up->cols);
     p.F = static_cast<int>(c.down->cols);
-    int rc = fill_mat(p.up, c.up, 2 * p.F);
-    if (rc == S12_OK) rc = fill_mat(p.down, c.down, p.H);
+    const int box_tiles = pl.small ? stage::kNT : 1, box_rows = pl.small ? stage::kRowsPerGroup : moe::kBlockRows;
+    int rc = fill_mat(p.up, c.up, 2 * p.F, box_tiles, box_rows);
+    if (rc == S12_OK) rc = fill_mat(p.down, c.down, p.H, box_tiles, box_rows);
     if (rc != S12_OK) return rc;
     p.x = c.x;
     p.router = c.router;
