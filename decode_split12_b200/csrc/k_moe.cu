@@ -1053,7 +1053,7 @@ constexpr int kUnits = 32;       // the queue; no warp is more than 16 tiles beh
 constexpr int kMaxRing = 8;      // stages
 constexpr int kBlockRows = 128;
 constexpr uint32_t kTileRaw = kBlockRows * kTile, kTileBytes = kTileRaw + kTileRaw / 2;
-constexpr uint32_t kSumCols = kSegLarge, kPlaceCols = kTile / 2;  // of TMEM: sums, decoded weights
+constexpr uint32_t kSumCols = 2 * kSegLarge, kPlaceCols = kTile / 2;  // of TMEM: sums, decoded weights
 constexpr uint32_t kTmemCols = 512;
 static_assert(2 * kSumCols + kGroups * kPlaceCols <= kTmemCols, "two places for sums, one for weights a group");
 
@@ -1193,7 +1193,7 @@ __device__ __forceinline__ void copy_step(const Params &p, LargeShared *sm, uint
             for (int i = 0; i < 2 * PH; ++i)  // 64 columns of a plane
                 asm volatile(
                     "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                        dst + i * atom),
+                        dst + ((i & 1) * PH + (i >> 1)) * atom),
                     "l"((PH == 1 ? p.xp : i >= 2 ? p.lo : p.hi) + src + (i & 1) * n * 128u), "r"(n * 128u), "r"(bar)
                     : "memory");
             ++c.x;
@@ -1247,7 +1247,7 @@ __device__ __forceinline__ void multiply_step(const Params &p, LargeShared *sm, 
     for (uint32_t ord = 0; ok; ++ord) {
         const Unit u = unit_at<PH>(p, sm, ord);
         if (u.n == 0) break;
-        const uint32_t n = product_pairs(sm->s.seg_n[u.seg]), idesc = product_desc(n), atom = n * 128u;
+        const uint32_t n = product_pairs(sm->s.seg_n[u.seg]), idesc = product_desc(PH * n), atom = PH * n * 128u;
         const uint32_t sums = tmem + (ord & 1u) * kSumCols;
         ok = mbar_wait_s(smem_addr(&sm->stored[PH - 1][ord & 1u]), ((ord >> 1) & 1u) ^ 1u);
         for (int t = 0; ok && t < u.n; ++t) {
@@ -1259,11 +1259,8 @@ __device__ __forceinline__ void multiply_step(const Params &p, LargeShared *sm, 
             const uint32_t wa = tmem + 2u * kSumCols + group * kPlaceCols;
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-#pragma unroll
-                for (int plane = 0; plane < PH; ++plane)
-                    umma_weights(sums, wa + k * 8,
-                                 tc::smem_desc_sw128(xa + (2 * plane + (k >> 2)) * atom + (k & 3) * 32u), idesc,
-                                 t == 0 && k == 0 && plane == 0 ? 0u : 1u);
+                umma_weights(sums, wa + k * 8, tc::smem_desc_sw128(xa + (k >> 2) * atom + (k & 3) * 32u), idesc,
+                             t == 0 && k == 0 ? 0u : 1u);
             tc::umma_commit(smem_addr(&sm->used[PH - 1][group]));
             tc::umma_commit(smem_addr(&sm->empty[PH - 1][slot]));
             if (t + 1 == u.n) tc::umma_commit(smem_addr(&sm->sums[PH - 1][group]));
@@ -1429,8 +1426,12 @@ __device__ __forceinline__ void decode_step(const Params &p, LargeShared *sm, ui
         if (known2) w2 = load_row<V, PH>(p, after, r);
         if (known) first_escape<V>(m, w1);
 
-        const bool ok = mbar_wait_s(smem_addr(&sm->weights[PH - 1][slot]), parity) &&
-                        mbar_wait_s(smem_addr(&sm->used[PH - 1][group]), gparity ^ 1u);
+        // (a wait tells a phase from its neighbours only, and this group meets a
+        // stage now and then: that its place was used shows that the stage's tile
+        // before last is done, that the stage was free that the last one is)
+        const bool ok = mbar_wait_s(smem_addr(&sm->used[PH - 1][group]), gparity ^ 1u) &&
+                        mbar_wait_s(smem_addr(&sm->empty[PH - 1][slot]), parity ^ 1u) &&
+                        mbar_wait_s(smem_addr(&sm->weights[PH - 1][slot]), parity);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
             lost(p, sm);
             return;
@@ -1468,13 +1469,17 @@ __device__ __forceinline__ void decode_step(const Params &p, LargeShared *sm, ui
             sparity ^= 1u;
             tc::tc_fence_after();
             for (int c = 0; c < pairs; c += 16) {
-                uint32_t v[4][4];
+                uint32_t v[PH][4][4];  // (of the high and the low part of h)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tc::tmem_ld4(from_sums + c + 4 * i, v[i]);
+                for (int i = 0; i < 4 * PH; ++i)
+                    tc::tmem_ld4(from_sums + (i >> 2) * product_pairs(pairs) + c + 4 * (i & 3), v[i >> 2][i & 3]);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c + i < pairs) __stcg(to + (c + i) * rows, __uint_as_float(v[i >> 2][i & 3]));
+                for (int i = 0; i < 16; ++i) {
+                    float sum = __uint_as_float(v[0][i >> 2][i & 3]);
+                    if (PH == 2) sum += __uint_as_float(v[PH - 1][i >> 2][i & 3]);
+                    if (c + i < pairs) __stcg(to + (c + i) * rows, sum);
+                }
             }
             tc::tc_fence_before();
             __syncwarp();
