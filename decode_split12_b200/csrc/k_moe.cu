@@ -1238,33 +1238,52 @@ __device__ __forceinline__ uint32_t product_desc(uint32_t n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((kBlockRows >> 4) << 24);
 }
 
-// A step by the thread that issues the products.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+// The value of lane 0, which makes it one for the warp in the compiler's eyes.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+// A step by the warp that issues the products.  It goes through the step as a
+// warp, and one lane issues: the operands of a product are then the warp's own
+// (by one lane alone, each was handed over anew: 122 cycles a product).
 template <int PH>
 __device__ __forceinline__ void multiply_step(const Params &p, LargeShared *sm, uint32_t base, uint32_t tmem) {
     const Stages rs = stages_of<PH>(p, sm, base);
+    const uint32_t stages = uniform(rs.n), bytes = uniform(rs.bytes), xs = uniform(rs.base) + kTileBytes;
+    const uint32_t places = uniform(tmem);
     uint32_t slot = 0, parity = 0, group = 0, gparity = 0;
     bool ok = true;
     for (uint32_t ord = 0; ok; ++ord) {
         const Unit u = unit_at<PH>(p, sm, ord);
-        if (u.n == 0) break;
-        const uint32_t n = product_pairs(sm->s.seg_n[u.seg]), idesc = product_desc(PH * n), atom = PH * n * 128u;
-        const uint32_t sums = tmem + (ord & 1u) * kSumCols;
+        const uint32_t tiles = uniform(static_cast<uint32_t>(u.n));
+        if (tiles == 0) break;
+        const uint32_t n = PH * uniform(product_pairs(sm->s.seg_n[u.seg])), idesc = product_desc(n);
+        const uint32_t sums = places + (ord & 1u) * kSumCols;
         ok = mbar_wait_s(smem_addr(&sm->stored[PH - 1][ord & 1u]), ((ord >> 1) & 1u) ^ 1u);
-        for (int t = 0; ok && t < u.n; ++t) {
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        for (uint32_t t = 0; ok && t < tiles; ++t) {
             ok = mbar_wait_s(smem_addr(&sm->x[PH - 1][slot]), parity) &&
                  mbar_wait_s(smem_addr(&sm->decoded[PH - 1][group]), gparity);
+            ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc::tc_fence_after();
-            const uint32_t xa = rs.base + slot * rs.bytes + kTileBytes;
-            const uint32_t wa = tmem + 2u * kSumCols + group * kPlaceCols;
+            const uint64_t x = tc::smem_desc_sw128(xs + slot * bytes);
+            const uint32_t wa = places + 2u * kSumCols + group * kPlaceCols;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-                umma_weights(sums, wa + k * 8, tc::smem_desc_sw128(xa + (k >> 2) * atom + (k & 3) * 32u), idesc,
-                             t == 0 && k == 0 ? 0u : 1u);
-            tc::umma_commit(smem_addr(&sm->used[PH - 1][group]));
-            tc::umma_commit(smem_addr(&sm->empty[PH - 1][slot]));
-            if (t + 1 == u.n) tc::umma_commit(smem_addr(&sm->sums[PH - 1][group]));
-            if (++slot == rs.n) {
+                for (uint32_t k = 0; k < kTile / 16; ++k)  // (the descriptor's address is in 16 bytes)
+                    umma_weights(sums, wa + k * 8, x + ((k >> 2) * n * 8u + (k & 3) * 2u), idesc,
+                                 k == 0 ? t != 0 : 1u);
+                tc::umma_commit(smem_addr(&sm->used[PH - 1][group]));
+                tc::umma_commit(smem_addr(&sm->empty[PH - 1][slot]));
+                if (t + 1 == tiles) tc::umma_commit(smem_addr(&sm->sums[PH - 1][group]));
+            }
+            __syncwarp();
+            if (++slot == stages) {
                 slot = 0;
                 parity ^= 1u;
             }
@@ -1276,7 +1295,8 @@ __device__ __forceinline__ void multiply_step(const Params &p, LargeShared *sm, 
     }
     if (!ok) lost(p, sm);
     // every product is over before its memory serves something else
-    tc::umma_commit(smem_addr(&sm->done[PH - 1]));
+    if (elect_one()) tc::umma_commit(smem_addr(&sm->done[PH - 1]));
+    __syncwarp();
     mbar_wait_s(smem_addr(&sm->done[PH - 1]), 0);
 }
 
@@ -1565,7 +1585,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_large_kernel(const __gri
             fence_for_copies();
             __syncthreads();
             Copied c1 = {0u, 0u}, c2 = {0u, 0u};
-            const bool copies = warp == 0 && lane == 0, multiplies = warp == 1 && lane == 0;
+            const bool copies = warp == 0 && lane == 0, multiplies = warp == 1;
             // the first weights are copied while the grid meets
             if (copies) c1 = copy_first<1>(p, sm, stages);
             __syncwarp();
