@@ -20,26 +20,35 @@
 // The first copies of step 2 are issued before the grid meets: weights do not
 // depend on it.
 //
-// Products.  As in the GEMV, a warp takes 16 rows x 2 tiles of weights a stage
-// from its own ring of two, decodes them in registers into the A operand of
-// mma.m16n8k16, and multiplies 8 tokens at a time.  (The tensor cores' own
-// kind of product reads its weights from shared memory, which the registers
-// would have to write first; at a few tokens its rate is not what is missing.)
-// Weights i and i + 4 of eight share a register, because their code nibbles
+// Two kernels share these steps, and a rule on the products' size chooses.
+// Small: as in the GEMV, a warp takes 16 rows x 2 tiles of weights a stage from
+// its own ring of two, decodes them in registers into the A operand of
+// mma.m16n8k16, and multiplies 8 tokens at a time; a warp waits for no other, and
+// a call starts fast.  Large: weights are decoded into TMEM and multiplied there
+// by up to 64 pairs (tcgen05), below.
+//
+// Decode.  Weights i and i + 4 of eight share a register, because their code nibbles
 // are 16 bits apart: a pair's exponents are one mask and one multiply-add of
 // the code word, its signs and mantissas one byte permute, and one bit select
 // joins them: 17 instructions for 8 weights.  x and h are kept with the same
 // pairs in a register.  h is kept as the sum of two BF16 values, so that it
 // carries 16 bits of mantissa and y is rounded once, where it is stored.
 //
-// Two kernels share these steps.  With few pairs an expert (4 on average, or at
-// most 8 tokens) x comes through L1 and warps take items one by one; with more
-// the warps of a CTA go through the same columns side by side, and x comes
-// through shared memory once for all of them.
-//
 // All sums have a fixed order, so y is the same on every call.  Every wait is
 // bounded.  One that gives up raises S12_FLAG_TIMEOUT and a word that the other
 // waits watch; the CTAs then leave, and the last one clears the words.
+//
+// Measured (5e-4 of the weights far outside their tiles' window; us, and the
+// experts' compressed bytes against a measured copy's 6.53 TB/s):
+//   8 experts of 14336 x 4096, top 2:  1 token 143 (0.58), 2 tokens 193 (0.64),
+//     8 tokens 420 (0.69), 16 tokens 503 (0.66), 64 tokens 515 (0.64)
+//   32 experts of 1408 x 2176, top 4:  1 token 50, 9 tokens 130 (0.45), 64 187 (0.37)
+//   64 experts of 1024 x 2048, top 8:  1 token 55, 16 tokens 165 (0.51), 64 192 (0.50)
+// A call of one token begins and ends in about 25 us (the choice of experts,
+// three meetings of the grid at 1.3 us, the sums).  Beyond that the small kernel
+// waits for the instructions that decode and multiply, the large one for those
+// that put escapes right and read metadata (without either 465 of the 515 us,
+// without both 382).
 #include <algorithm>
 #include <type_traits>
 
@@ -181,8 +190,8 @@ __device__ __forceinline__ bool grid_meet(const Params &p, Shared *sm, int word)
 template <bool LARGE>
 __device__ __forceinline__ void pack_piece(const Params &p, uint8_t *to, int t, int c8, int n, int i) {
     const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(t) * p.H) + c8);
-    *reinterpret_cast<uint4 *>(to + piece_of<LARGE>(c8, n, i)) = make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u),
-                      prmt(v.y, v.w, 0x7632u));
+    *reinterpret_cast<uint4 *>(to + piece_of<LARGE>(c8, n, i)) = make_uint4(
+        prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u), prmt(v.y, v.w, 0x7632u));
 }
 
 // x token by token.
@@ -514,18 +523,13 @@ __device__ __forceinline__ void load_x(uint32_t (&xw)[8], const uint8_t *src, si
     xw[4] = b.x; xw[5] = b.y; xw[6] = b.z; xw[7] = b.w;
 }
 
-// The chunk's four products with each of N eights of tokens.  A product waits
-// for the one before it on the same sums, so neighbours have sums of their own:
-// acc[n] over the eights (N > 1), or four chains for one eight.
-template <int N, int A>
-__device__ __forceinline__ void chunk_mma(float (&acc)[A][4], int n0, const uint32_t (&wa)[8], const uint32_t (&wb)[8],
-                                          const uint32_t (&xw)[N][8]) {
+// The chunk's four products.  One would wait for the one before it on the same
+// sums, so each has sums of its own.
+__device__ __forceinline__ void chunk_mma(float (&acc)[4][4], const uint32_t (&wa)[8], const uint32_t (&wb)[8],
+                                          const uint32_t (&xw)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-            mma16816(acc[N == 1 ? i : n0 + n], wa[2 * i], wb[2 * i], wa[2 * i + 1], wb[2 * i + 1], xw[n][2 * i],
-                     xw[n][2 * i + 1]);
+        mma16816(acc[i], wa[2 * i], wb[2 * i], wa[2 * i + 1], wb[2 * i + 1], xw[2 * i], xw[2 * i + 1]);
 }
 
 // ---------------------------------------------------------------------------
@@ -761,8 +765,10 @@ __device__ __forceinline__ void stage_products(const Params &p, const Mat &m, co
         decode_pairs(rB.z, rB.w, c & 1 ? kB.w : kB.y, B2B, wb + 4);
         if (patches) {
             const uint32_t hereA = (nA >> (8 * c)) & 0xFFu, hereB = (nB >> (8 * c)) & 0xFFu;
-            if (hereA) patch(wa, c & 1 ? make_uint2(kA.z, kA.w) : make_uint2(kA.x, kA.y), iA, limA, knownA, evA, m.esc, p.err);
-            if (hereB) patch(wb, c & 1 ? make_uint2(kB.z, kB.w) : make_uint2(kB.x, kB.y), iB, limB, knownB, evB, m.esc, p.err);
+            const uint2 CA = c & 1 ? make_uint2(kA.z, kA.w) : make_uint2(kA.x, kA.y);
+            const uint2 CB = c & 1 ? make_uint2(kB.z, kB.w) : make_uint2(kB.x, kB.y);
+            if (hereA) patch(wa, CA, iA, limA, knownA, evA, m.esc, p.err);
+            if (hereB) patch(wb, CB, iB, limB, knownB, evB, m.esc, p.err);
             iA += hereA;
             iB += hereB;
         }
@@ -817,13 +823,13 @@ __device__ __forceinline__ bool small_step(const Params &p, const SmallShared *s
         Desc d2;
         d2.live = false;
         auto multiply = [&](int c, const uint32_t (&wa)[8], const uint32_t (&wb)[8]) {
-            uint32_t xw[1][8];
+            uint32_t xw[8];
             const uint8_t *src = xl + at + c * chunk_bytes;
-            load_x(xw[0], src, half, live);
-            chunk_mma(acc, 0, wa, wb, xw);
+            load_x(xw, src, half, live);
+            chunk_mma(acc, wa, wb, xw);
             if (PH == 2) {
-                load_x(xw[0], src + lo, half, live);
-                chunk_mma(acc, 0, wa, wb, xw);
+                load_x(xw, src + lo, half, live);
+                chunk_mma(acc, wa, wb, xw);
             }
         };
         auto refill = [&]() {
@@ -1031,31 +1037,38 @@ __global__ void __launch_bounds__(kThreads, 1) moe_small_kernel(const __grid_con
 // A unit is a block of 128 rows of a segment's expert by a range of columns:
 // D[row][pair] += W[row][k] * x[pair][k] on the tcgen05 tensor cores, 128 columns
 // (a tile of each row) at a time.  W is the product's left side and is kept in
-// TMEM, where the threads that decode it write it from registers: a thread has
-// one row of the tile, which is one lane of TMEM.  (Through mma.sync, as above,
-// every warp reads all of x from shared memory for 16 rows of weights: 64 tokens
-// of 8 experts of 14336 x 4096 took 815 us.)  x and h are copied to shared
-// memory as the product wants them (128-byte swizzle).
+// TMEM, where the threads that decode it write it from registers: a row of the
+// tile is a lane of TMEM.  (Through mma.sync, every warp reads all of x from
+// shared memory for 16 rows of weights: 64 tokens of 8 experts of 14336 x 4096
+// took 815 us, against 515.)  x and h are copied to shared memory as the product
+// wants them (128-byte swizzle).  h's high and low parts are one product of twice
+// the width, whose halves are added where the sums are stored: a product takes as
+// long for 64 columns as for 32 (two in a row: 607 us, one: 573).
 //
 // Warp 0 claims units and copies weights and x into a ring of stages, a tile
-// each; warp 1 issues the products; sixteen warps decode, four to a tile, each
-// four with a place in TMEM of their own.  The four that had a unit's last tile
-// store its sums, while the other twelve decode the next unit's tiles (there are
-// two places for sums).  Every wait is for something of an earlier tile, or of
-// an earlier part of the same tile, so the tiles' order shows that all end.
-// Units come from a counter of the grid as items do above; the first weights of
-// a step are copied while the grid meets.
+// each; warp 1 issues the products; sixteen warps decode, eight to a tile, which
+// holds a stage half as long as four do; two warps read a unit's metadata ahead,
+// a row's tiles side by side (read by the thread that has the row, every word is
+// a sector of its own, and the loads took a fifth of the decoding warps' time).
+// The eight warps that had a unit's last tile store its sums, while the others
+// decode the next unit's tiles (there are two places for sums).  Every wait is
+// for something of an earlier tile, or of an earlier part of the same tile, so
+// the tiles' order shows that all end.  Units come from a counter of the grid as
+// items do above; the first weights of a step are copied while the grid meets.
 
-constexpr int kGroups = 4;       // of four warps that decode a tile
-constexpr int kLargeThreads = 32 * (2 + 4 * kGroups);
+constexpr int kGroups = 2, kGroupWarps = 8;  // warps that decode a tile: four, by rows, for each half of its columns
+constexpr int kPlaces = 2 * kGroups;         // of decoded weights
+constexpr int kDecodeWarps = kGroups * kGroupWarps, kMetaWarps = 2;
+constexpr int kLargeThreads = 32 * (2 + kDecodeWarps + kMetaWarps);
+constexpr int kUnitTiles = 16;   // tiles of a unit at most
 constexpr int kAhead = 3;        // units that a CTA knows in advance
-constexpr int kUnits = 32;       // the queue; no warp is more than 16 tiles behind the copies
+constexpr int kUnits = 32;       // the queue: no warp is more than 16 tiles behind the copies
 constexpr int kMaxRing = 8;      // stages
 constexpr int kBlockRows = 128;
 constexpr uint32_t kTileRaw = kBlockRows * kTile, kTileBytes = kTileRaw + kTileRaw / 2;
 constexpr uint32_t kSumCols = 2 * kSegLarge, kPlaceCols = kTile / 2;  // of TMEM: sums, decoded weights
 constexpr uint32_t kTmemCols = 512;
-static_assert(2 * kSumCols + kGroups * kPlaceCols <= kTmemCols, "two places for sums, one for weights a group");
+static_assert(2 * kSumCols + kPlaces * kPlaceCols <= kTmemCols, "two places for sums, two for weights a group");
 
 struct LargeShared {
     Shared s;
@@ -1063,9 +1076,12 @@ struct LargeShared {
     unsigned long long queue[2][kUnits];  // ordinal << 32 | unit
     // mbarriers, by step
     unsigned long long weights[2][kMaxRing], x[2][kMaxRing], empty[2][kMaxRing];  // stages: copied, free
-    unsigned long long decoded[2][kGroups], used[2][kGroups];                     // places of decoded weights
+    unsigned long long decoded[2][kPlaces], used[2][kPlaces];                     // places of decoded weights
     unsigned long long sums[2][kGroups], stored[2][2];  // a group's last tile multiplied; places of sums free
-    unsigned long long done[2];                                                   // all products of the step
+    unsigned long long read[2][2], spent[2][2];          // a unit's metadata
+    unsigned long long done[2];                          // all products of the step
+    uint2 meta[2][kUnitTiles * (kBlockRows + 1)];        // of the tile rows of two units
+    uint32_t tally[kPlaces][kBlockRows];                 // escapes found in a tile row by the half done first
     uint32_t tmem, abort;
 };
 
@@ -1254,42 +1270,42 @@ template <int PH>
 __device__ __forceinline__ void multiply_step(const Params &p, LargeShared *sm, uint32_t base, uint32_t tmem) {
     const Stages rs = stages_of<PH>(p, sm, base);
     const uint32_t stages = uniform(rs.n), bytes = uniform(rs.bytes), xs = uniform(rs.base) + kTileBytes;
-    const uint32_t places = uniform(tmem);
-    uint32_t slot = 0, parity = 0, group = 0, gparity = 0;
+    const uint32_t tm = uniform(tmem);
+    uint32_t slot = 0, parity = 0, place = 0, pparity = 0;
     bool ok = true;
     for (uint32_t ord = 0; ok; ++ord) {
         const Unit u = unit_at<PH>(p, sm, ord);
         const uint32_t tiles = uniform(static_cast<uint32_t>(u.n));
         if (tiles == 0) break;
         const uint32_t n = PH * uniform(product_pairs(sm->s.seg_n[u.seg])), idesc = product_desc(n);
-        const uint32_t sums = places + (ord & 1u) * kSumCols;
+        const uint32_t sums = tm + (ord & 1u) * kSumCols;
         ok = mbar_wait_s(smem_addr(&sm->stored[PH - 1][ord & 1u]), ((ord >> 1) & 1u) ^ 1u);
         ok = __all_sync(0xFFFFFFFFu, ok);
         for (uint32_t t = 0; ok && t < tiles; ++t) {
             ok = mbar_wait_s(smem_addr(&sm->x[PH - 1][slot]), parity) &&
-                 mbar_wait_s(smem_addr(&sm->decoded[PH - 1][group]), gparity);
+                 mbar_wait_s(smem_addr(&sm->decoded[PH - 1][place]), pparity);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc::tc_fence_after();
             const uint64_t x = tc::smem_desc_sw128(xs + slot * bytes);
-            const uint32_t wa = places + 2u * kSumCols + group * kPlaceCols;
+            const uint32_t wa = tm + 2u * kSumCols + place * kPlaceCols;
             if (elect_one()) {
 #pragma unroll
                 for (uint32_t k = 0; k < kTile / 16; ++k)  // (the descriptor's address is in 16 bytes)
                     umma_weights(sums, wa + k * 8, x + ((k >> 2) * n * 8u + (k & 3) * 2u), idesc,
                                  k == 0 ? t != 0 : 1u);
-                tc::umma_commit(smem_addr(&sm->used[PH - 1][group]));
+                tc::umma_commit(smem_addr(&sm->used[PH - 1][place]));
                 tc::umma_commit(smem_addr(&sm->empty[PH - 1][slot]));
-                if (t + 1 == tiles) tc::umma_commit(smem_addr(&sm->sums[PH - 1][group]));
+                if (t + 1 == tiles) tc::umma_commit(smem_addr(&sm->sums[PH - 1][place % kGroups]));
             }
             __syncwarp();
             if (++slot == stages) {
                 slot = 0;
                 parity ^= 1u;
             }
-            if (++group == kGroups) {
-                group = 0;
-                gparity ^= 1u;
+            if (++place == kPlaces) {
+                place = 0;
+                pparity ^= 1u;
             }
         }
     }
@@ -1300,185 +1316,219 @@ __device__ __forceinline__ void multiply_step(const Params &p, LargeShared *sm, 
     mbar_wait_s(smem_addr(&sm->done[PH - 1]), 0);
 }
 
-// A group's way through a step: every fourth tile, across units.
-struct Way {
-    uint32_t ord, row;
-    int j, k, n;  // the unit's first tile, the tile in it, its tiles (0: the end)
-};
-
-template <int PH>
-__device__ __forceinline__ void enter(const Params &p, const LargeShared *sm, Way &w, const Unit &u) {
-    w.n = u.n;
-    w.j = u.j;
-    if (u.n) w.row = row_of<PH>(p, sm, u);
+// What decoding a tile row takes: x: its first escape's place; y: base | number
+// of escapes << 8 | the first escape << 16.  (No tile row has more than 128;
+// above 254 the metadata is wrong, as where it ends before it starts: 255.)
+__device__ __forceinline__ uint2 meta_word(uint32_t base, uint32_t from, uint32_t end, uint32_t ev) {
+    const uint32_t n = from <= end ? min(end - from, 254u) : 255u;
+    return make_uint2(from, (base & 0xFFu) | (n << 8) | (ev << 16));
 }
 
-// The way `tiles` on; false (and w as it was) when a unit is not known yet.
-template <int PH, bool WAIT>
-__device__ __forceinline__ bool go(const Params &p, LargeShared *sm, Way &w, int tiles) {
-    Way to = w;
-    to.k += tiles;
-    while (to.n && to.k >= to.n) {
-        to.k -= to.n;
-        ++to.ord;
-        Unit u;
-        if (WAIT)
-            u = unit_at<PH>(p, sm, to.ord);
-        else if (!peek<PH>(p, sm, to.ord, u))
-            return false;
-        enter<PH>(p, sm, to, u);
-    }
-    w = to;
-    return true;
-}
-
-// Metadata of the thread's tile row, as loaded words.
-struct RowWords {
-    uint32_t w0, w1, w2, w3;  // version 1: base, esc_off[t], esc_off[t + 1], its first escape (later);
-                              // version 2: tmeta[t], and of the three tiles before that are in the unit
-};
-
+// A step by a warp that reads metadata: half of a unit's rows, two at a time, a
+// lane for each of 16 tiles.
 template <int V, int PH>
-__device__ __forceinline__ RowWords load_row(const Params &p, const Way &w, int r) {
+__device__ __forceinline__ void meta_step(const Params &p, LargeShared *sm) {
+    constexpr int kRows = kBlockRows / kMetaWarps, kBatch = 8;
     const Mat &m = mat<PH>(p);
-    RowWords o = {0u, 0u, 0u, 0u};
-    if (w.n == 0) return o;
-    const size_t at = static_cast<size_t>(w.row + r) * m.T + w.j + w.k;
-    if (V == 1) {
-        o.w0 = __ldg(static_cast<const uint8_t *>(m.meta) + at);
-        o.w1 = __ldg(m.off + at);
-        o.w2 = __ldg(m.off + at + 1);
-    } else {
-        const uint16_t *tm = static_cast<const uint16_t *>(m.meta) + at;
-        o.w0 = __ldg(tm);
-        if (w.k >= 1) o.w1 = __ldg(tm - 1);
-        if (w.k >= 2) o.w2 = __ldg(tm - 2);
-        if (w.k >= 3) o.w3 = __ldg(tm - 3);
+    const int lane = threadIdx.x & 31, t = lane & 15;
+    const int r0 = (static_cast<int>(threadIdx.x >> 5) - 2 - kDecodeWarps) * kRows + (lane >> 4);
+    for (uint32_t ord = 0;; ++ord) {
+        const Unit u = unit_at<PH>(p, sm, ord);
+        if (u.n == 0) break;
+        const uint32_t d = ord & 1u;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_s(smem_addr(&sm->spent[PH - 1][d]), ((ord >> 1) & 1u) ^ 1u))) {
+            lost(p, sm);
+            return;
+        }
+        const size_t row = row_of<PH>(p, sm, u);
+#pragma unroll 1
+        for (int i0 = 0; i0 < kRows; i0 += 2 * kBatch) {
+            uint32_t base[kBatch], from[kBatch], end[kBatch], ev[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const size_t r = row + r0 + i0 + 2 * b, at = r * m.T + u.j + t;
+                base[b] = from[b] = end[b] = ev[b] = 0u;
+                if (V == 1) {
+                    if (t < u.n) {
+                        base[b] = __ldg(static_cast<const uint8_t *>(m.meta) + at);
+                        from[b] = __ldg(m.off + at);
+                        end[b] = __ldg(m.off + at + 1);
+                    }
+                } else {
+                    // row_esc and the counts of the row's earlier tiles
+                    const uint16_t *tm = static_cast<const uint16_t *>(m.meta) + r * m.T;
+                    for (int k = t; k < u.j; k += 16) from[b] += __ldg(tm + k) >> 8;
+                    if (t < u.n) base[b] = __ldg(tm + u.j + t);
+                    end[b] = __ldg(m.off + r);
+                }
+            }
+            if (V == 2) {
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    uint32_t before = from[b], upto = base[b] >> 8;
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) {
+                        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o, 16);
+                        if (t >= o) upto += v;
+                    }
+                    end[b] += before + upto;
+                    from[b] = end[b] - (base[b] >> 8);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (from[b] < end[b] && from[b] < m.n_esc) ev[b] = __ldg(m.esc + from[b]);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                sm->meta[d][t * (kBlockRows + 1) + r0 + i0 + 2 * b] = meta_word(base[b], from[b], end[b], ev[b]);
+        }
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(smem_addr(&sm->read[PH - 1][d]));
     }
-    return o;
 }
 
-template <int V>
-__device__ __forceinline__ void first_escape(const Mat &m, RowWords &w) {
-    if (V == 1 && w.w1 != w.w2 && w.w1 < m.n_esc) w.w3 = __ldg(m.esc + w.w1);
-}
-
-// Version 2: escapes of a row before tile j.
-__device__ __forceinline__ uint32_t escapes_before(const Mat &m, size_t row, int j) {
-    const uint16_t *tm = static_cast<const uint16_t *>(m.meta) + row * m.T;
-    uint32_t n = __ldg(m.off + row);
-#pragma unroll 16
-    for (int t = 0; t < j; ++t) n += __ldg(tm + t) >> 8;
-    return n;
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[2][8]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        "r"(v[0][0]), "r"(v[0][1]), "r"(v[0][2]), "r"(v[0][3]), "r"(v[0][4]), "r"(v[0][5]), "r"(v[0][6]), "r"(v[0][7]),
+        "r"(v[1][0]), "r"(v[1][1]), "r"(v[1][2]), "r"(v[1][3]), "r"(v[1][4]), "r"(v[1][5]), "r"(v[1][6]), "r"(v[1][7])
         : "memory");
 }
 
-// The thread's row (r of the block) of a tile: its 128 weights to its lane of TMEM.
-template <int V>
-__device__ __forceinline__ void decode_row(const Params &p, const Mat &m, uint32_t st, uint32_t to, int r, uint32_t base,
-                                           uint32_t from, uint32_t end, uint32_t ev) {
+// Half of the thread's row (r of the block) of a tile: 64 weights to its lane of
+// TMEM.  The first half counts the row's escapes up from the first, the second
+// down from the last; `tally` brings the two numbers together.
+template <bool UP>
+__device__ __forceinline__ void decode_half(const Params &p, const Mat &m, uint32_t st, uint32_t to, int r, uint2 w,
+                                            uint32_t *tally) {
+    const uint32_t base = w.y & 0xFFu, count = (w.y >> 8) & 0xFFu;
     if (p.err && base > static_cast<uint32_t>(kMaxBase)) raise_flag(p.err, S12_FLAG_BASE);
     const uint32_t raw = st + static_cast<uint32_t>(r) * 128u, rsw = static_cast<uint32_t>(r) & 7u;
     const uint32_t code = st + kTileRaw + static_cast<uint32_t>(r) * 64u, csw = (static_cast<uint32_t>(r) >> 1) & 3u;
-    const uint32_t B2 = base * 0x00800080u, limit = from <= end ? min(end, m.n_esc) : 0u;
-    const uint32_t known = V == 1 ? from : ~0u;
-    uint32_t idx = from;
+    const uint32_t B2 = base * 0x00800080u, marks = count ? 0x88888888u : 0u;
+    const uint32_t n = count == 255u ? 0u : count, limit = min(w.x + n, m.n_esc);
+    const uint32_t first = UP ? w.x : w.x + n - 1u;
+    uint32_t idx = first;
+    // the exact values of a word's escapes (most rows with any have one)
+    auto exact = [&](uint32_t mm, uint32_t *v) {
+        while (mm) {
+            const uint32_t j = static_cast<uint32_t>(UP ? __ffs(static_cast<int>(mm)) - 1 : 31 - __clz(mm)) >> 2;
+            mm &= ~(8u << (4u * j));
+            uint32_t value = 0;
+            if (idx - w.x < n && idx < limit)
+                value = idx == w.x ? w.y >> 16 : __ldg(m.esc + idx);
+            else
+                raise_flag(p.err, S12_FLAG_ESC_RANGE);
+            idx += UP ? 1u : ~0u;
+            const uint32_t sel = j & 4u ? 0x5410u : 0x3254u;
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) v[i] = prmt(v[i], value, i == (j & 3u) ? sel : 0x3210u);
+        }
+    };
 #pragma unroll 1
-    for (uint32_t c = 0; c < 4; ++c) {  // 32 columns
+    for (uint32_t i = 0; i < 2; ++i) {  // 32 columns
+        const uint32_t c = UP ? i : 3u - i;
         const uint4 k = lds128(code + ((c ^ csw) << 4));
         const uint4 a = lds128(raw + (((2u * c) ^ rsw) << 4)), b = lds128(raw + (((2u * c + 1u) ^ rsw) << 4));
-        uint32_t w[2][8];
-        decode_pairs(a.x, a.y, k.x, B2, w[0]);
-        decode_pairs(a.z, a.w, k.y, B2, w[0] + 4);
-        decode_pairs(b.x, b.y, k.z, B2, w[1]);
-        decode_pairs(b.z, b.w, k.w, B2, w[1] + 4);
-        if (from != end) {
-            const uint32_t n0 = __popc(escape_nibbles(k.x)) + __popc(escape_nibbles(k.y));
-            const uint32_t n1 = __popc(escape_nibbles(k.z)) + __popc(escape_nibbles(k.w));
-            if (n0) patch(w[0], make_uint2(k.x, k.y), idx, limit, known, ev, m.esc, p.err);
-            idx += n0;
-            if (n1) patch(w[1], make_uint2(k.z, k.w), idx, limit, known, ev, m.esc, p.err);
-            idx += n1;
+        uint32_t v[2][8];
+        decode_pairs(a.x, a.y, k.x, B2, v[0]);
+        decode_pairs(a.z, a.w, k.y, B2, v[0] + 4);
+        decode_pairs(b.x, b.y, k.z, B2, v[1]);
+        decode_pairs(b.z, b.w, k.w, B2, v[1] + 4);
+        const uint32_t m0 = escape_nibbles(k.x) & marks, m1 = escape_nibbles(k.y) & marks;
+        const uint32_t m2 = escape_nibbles(k.z) & marks, m3 = escape_nibbles(k.w) & marks;
+        if (m0 | m1 | m2 | m3) {
+            if (UP) {
+                exact(m0, v[0]);
+                exact(m1, v[0] + 4);
+                exact(m2, v[1]);
+                exact(m3, v[1] + 4);
+            } else {
+                exact(m3, v[1] + 4);
+                exact(m2, v[1]);
+                exact(m1, v[0] + 4);
+                exact(m0, v[0]);
+            }
         }
         __syncwarp();
-        uint32_t v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = w[i >> 3][i & 7];
         tmem_st16(to + c * 16u, v);
     }
-    if (idx != end && p.err) raise_flag(p.err, S12_FLAG_ESC_COUNT);
+    if (count && p.err) {
+        const uint32_t found = UP ? idx - first : first - idx;
+        const uint32_t other = atomicAdd(tally, 0x10000u | found);
+        if (other) {
+            if ((other & 0xFFFFu) + found != count) raise_flag(p.err, S12_FLAG_ESC_COUNT);
+            *tally = 0u;
+        }
+    }
 }
 
-// A step by one of the warps that decode.
-template <int V, int PH>
+// A step by one of the warps that decode: every other tile, across units.
+template <int PH>
 __device__ __forceinline__ void decode_step(const Params &p, LargeShared *sm, uint32_t base, uint32_t tmem) {
     const Mat &m = mat<PH>(p);
     const Stages rs = stages_of<PH>(p, sm, base);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = (warp - 2) >> 2, quad = warp & 3;
-    const int r = quad * 32 + lane;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = (warp - 2) / kGroupWarps, quad = warp & 3;
+    const int r = quad * 32 + lane, half = ((warp - 2) >> 2) & 1;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;  // TMEM lanes 32 quad on are this warp's
-    const uint32_t place = tmem + lanes + 2u * kSumCols + static_cast<uint32_t>(group) * kPlaceCols;
-    uint32_t slot = static_cast<uint32_t>(group), parity = 0, gparity = 0, sparity = 0, run = 0;
-    Way at = {0u, 0u, 0, 0, 0}, next;
-    enter<PH>(p, sm, at, unit_at<PH>(p, sm, 0));
-    go<PH, true>(p, sm, at, group);
-    RowWords w0 = load_row<V, PH>(p, at, r), w1 = {0u, 0u, 0u, 0u}, w2 = w1;
-    first_escape<V>(m, w0);
-    next = at;
-    bool known = false;  // `next` is the tile after this one, and w1 its words
-    while (at.n) {
-        while (slot >= rs.n) {
-            slot -= rs.n;
-            parity ^= 1u;
+    uint32_t slot = static_cast<uint32_t>(group), parity = 0, sparity = 0;
+    uint32_t place = static_cast<uint32_t>(group), pparity = 0;
+    int k = group;  // the next tile, counted from the unit's first
+    for (uint32_t ord = 0;; ++ord) {
+        const Unit u = unit_at<PH>(p, sm, ord);
+        if (u.n == 0) break;
+        const uint32_t d = ord & 1u;
+        bool ok = mbar_wait_s(smem_addr(&sm->read[PH - 1][d]), (ord >> 1) & 1u);
+        for (; k < u.n; k += kGroups) {
+            while (slot >= rs.n) {
+                slot -= rs.n;
+                parity ^= 1u;
+            }
+            // (a wait tells a phase from its neighbours only, and this group meets a
+            // stage now and then: that its place was used shows that the stage's tile
+            // before last is done, that the stage was free that the last one is)
+            ok = ok && mbar_wait_s(smem_addr(&sm->used[PH - 1][place]), pparity ^ 1u) &&
+                 mbar_wait_s(smem_addr(&sm->empty[PH - 1][slot]), parity ^ 1u) &&
+                 mbar_wait_s(smem_addr(&sm->weights[PH - 1][slot]), parity);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                lost(p, sm);
+                return;
+            }
+            tc::tc_fence_after();
+            const uint2 w = sm->meta[d][k * (kBlockRows + 1) + r];
+            const uint32_t st = rs.base + slot * rs.bytes, to = tmem + lanes + 2u * kSumCols + place * kPlaceCols;
+            if (half)
+                decode_half<false>(p, m, st, to, r, w, &sm->tally[place][r]);
+            else
+                decode_half<true>(p, m, st, to, r, w, &sm->tally[place][r]);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                tc::bar_arrive(smem_addr(&sm->decoded[PH - 1][place]));
+                tc::bar_arrive(smem_addr(&sm->empty[PH - 1][slot]));
+            }
+            slot += kGroups;
+            place += kGroups;
+            if (place >= kPlaces) {
+                place -= kPlaces;
+                pparity ^= 1u;
+            }
         }
-        // two tiles ahead: a tile's words, one ahead: the escape they point to
-        if (!known && (known = go<PH, false>(p, sm, next, kGroups))) w1 = load_row<V, PH>(p, next, r);
-        Way after = next;
-        const bool known2 = known && go<PH, false>(p, sm, after, kGroups);
-        if (known2) w2 = load_row<V, PH>(p, after, r);
-        if (known) first_escape<V>(m, w1);
-
-        // (a wait tells a phase from its neighbours only, and this group meets a
-        // stage now and then: that its place was used shows that the stage's tile
-        // before last is done, that the stage was free that the last one is)
-        const bool ok = mbar_wait_s(smem_addr(&sm->used[PH - 1][group]), gparity ^ 1u) &&
-                        mbar_wait_s(smem_addr(&sm->empty[PH - 1][slot]), parity ^ 1u) &&
-                        mbar_wait_s(smem_addr(&sm->weights[PH - 1][slot]), parity);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
             lost(p, sm);
             return;
         }
-        tc::tc_fence_after();
-        uint32_t from = w0.w1, end = w0.w2;
-        if (V == 2) {
-            if (at.k < kGroups) run = escapes_before(m, at.row + r, at.j);
-            from = run + (w0.w1 >> 8) + (w0.w2 >> 8) + (w0.w3 >> 8);
-            run = end = from + (w0.w0 >> 8);
-        }
-        decode_row<V>(p, m, rs.base + slot * rs.bytes, place, r, V == 1 ? w0.w0 : w0.w0 & 0xFFu, from, end, w0.w3);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-            tc::bar_arrive(smem_addr(&sm->decoded[PH - 1][group]));
-            tc::bar_arrive(smem_addr(&sm->empty[PH - 1][slot]));
-        }
-        gparity ^= 1u;
-        slot += kGroups;
-        if (at.k + 1 == at.n) {
-            // the unit's sums, a lane of TMEM for each row
-            const Unit u = unit_at<PH>(p, sm, at.ord);
+        if (lane == 0) tc::bar_arrive(smem_addr(&sm->spent[PH - 1][d]));
+        k -= u.n;
+        if (k == kGroups - 1) {
+            // the unit's last tile was this group's: its sums, a lane of TMEM for each row
             const int pairs = sm->s.seg_n[u.seg];
             const size_t rows = static_cast<size_t>(m.G) * kRowsPerGroup;  // of an expert
-            const uint32_t d = at.ord & 1u, from_sums = tmem + lanes + d * kSumCols;
+            const uint32_t sums = tmem + lanes + d * kSumCols;
             float *to = (PH == 1 ? p.gu : p.d) +
                         (static_cast<size_t>(u.range) * (p.tokens * p.top_k) + sm->s.seg_first[u.seg]) * rows +
                         static_cast<size_t>(u.block) * kBlockRows + r;
@@ -1488,14 +1538,14 @@ __device__ __forceinline__ void decode_step(const Params &p, LargeShared *sm, ui
             }
             sparity ^= 1u;
             tc::tc_fence_after();
-            for (int c = 0; c < pairs; c += 16) {
-                uint32_t v[PH][4][4];  // (of the high and the low part of h)
+            for (int c = 8 * half; c < pairs; c += 16) {
+                uint32_t v[PH][2][4];  // (of the high and the low part of h)
 #pragma unroll
-                for (int i = 0; i < 4 * PH; ++i)
-                    tc::tmem_ld4(from_sums + (i >> 2) * product_pairs(pairs) + c + 4 * (i & 3), v[i >> 2][i & 3]);
+                for (int i = 0; i < 2 * PH; ++i)
+                    tc::tmem_ld4(sums + (i >> 1) * product_pairs(pairs) + c + 4 * (i & 1), v[i >> 1][i & 1]);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     float sum = __uint_as_float(v[0][i >> 2][i & 3]);
                     if (PH == 2) sum += __uint_as_float(v[PH - 1][i >> 2][i & 3]);
                     if (c + i < pairs) __stcg(to + (c + i) * rows, sum);
@@ -1504,18 +1554,6 @@ __device__ __forceinline__ void decode_step(const Params &p, LargeShared *sm, ui
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::bar_arrive(smem_addr(&sm->stored[PH - 1][d]));
-        }
-        if (known) {
-            at = next;
-            w0 = w1;
-            next = after;
-            w1 = w2;
-            known = known2;
-        } else {
-            go<PH, true>(p, sm, at, kGroups);
-            w0 = load_row<V, PH>(p, at, r);
-            first_escape<V>(m, w0);
-            next = at;
         }
     }
 }
@@ -1535,19 +1573,24 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_large_kernel(const __gri
             for (int s = 0; s < kMaxRing; ++s) {
                 mbar_init_s(smem_addr(&sm->weights[i][s]), 1);
                 mbar_init_s(smem_addr(&sm->x[i][s]), 1);
-                mbar_init_s(smem_addr(&sm->empty[i][s]), 4 + 1);  // the warps that decode it, the products
+                mbar_init_s(smem_addr(&sm->empty[i][s]), kGroupWarps + 1);  // the warps that decode it, the products
             }
-            for (int g = 0; g < kGroups; ++g) {
-                mbar_init_s(smem_addr(&sm->decoded[i][g]), 4);
-                mbar_init_s(smem_addr(&sm->used[i][g]), 1);
-                mbar_init_s(smem_addr(&sm->sums[i][g]), 1);
+            for (int k = 0; k < kPlaces; ++k) {
+                mbar_init_s(smem_addr(&sm->decoded[i][k]), kGroupWarps);
+                mbar_init_s(smem_addr(&sm->used[i][k]), 1);
             }
-            for (int d = 0; d < 2; ++d) mbar_init_s(smem_addr(&sm->stored[i][d]), 4);
+            for (int g = 0; g < kGroups; ++g) mbar_init_s(smem_addr(&sm->sums[i][g]), 1);
+            for (int d = 0; d < 2; ++d) {
+                mbar_init_s(smem_addr(&sm->stored[i][d]), kGroupWarps);
+                mbar_init_s(smem_addr(&sm->read[i][d]), kMetaWarps);
+                mbar_init_s(smem_addr(&sm->spent[i][d]), kDecodeWarps);
+            }
             mbar_init_s(smem_addr(&sm->done[i]), 1);
         }
         sm->abort = 0u;
         fence_barrier_init();
     }
+    for (int i = threadIdx.x; i < kPlaces * kBlockRows; i += blockDim.x) (&sm->tally[0][0])[i] = 0u;
     if (warp == 1) {
         tc::tmem_alloc(smem_addr(&sm->tmem), kTmemCols);
         tc::tmem_relinquish();
@@ -1596,8 +1639,10 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_large_kernel(const __gri
                     if (!*const_cast<volatile uint32_t *>(&sm->abort)) c2 = copy_first<2>(p, sm, stages);
                 } else if (multiplies) {
                     multiply_step<1>(p, sm, stages, tmem);
+                } else if (warp >= 2 + kDecodeWarps) {
+                    meta_step<V, 1>(p, sm);
                 } else if (warp >= 2) {
-                    decode_step<V, 1>(p, sm, stages, tmem);
+                    decode_step<1>(p, sm, stages, tmem);
                 }
                 __syncwarp();
                 if (grid_meet(p, &sm->s, kBarSums)) {
@@ -1612,8 +1657,10 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_large_kernel(const __gri
                                 copy_step<2>(p, sm, stages, c2);
                             } else if (multiplies) {
                                 multiply_step<2>(p, sm, stages, tmem);
+                            } else if (warp >= 2 + kDecodeWarps) {
+                                meta_step<V, 2>(p, sm);
                             } else if (warp >= 2) {
-                                decode_step<V, 2>(p, sm, stages, tmem);
+                                decode_step<2>(p, sm, stages, tmem);
                             }
                         }
                         __syncwarp();
@@ -1644,10 +1691,11 @@ namespace {
 
 constexpr uint32_t kSmemLimit = 227 * 1024;
 
-// Stages of an item.  Few pairs: 2, 4 and 8 took 139, 129 and 133 us for a layer
-// of 8 experts of 14336 x 4096 and one token; shorter ones cost more work an
-// item, longer ones leave SMs idle at a step's end.
-constexpr uint32_t kRangeSmall = 4, kRangeLarge = 8;
+// Stages of an item.  Shorter ones cost more work an item, longer ones leave SMs
+// idle at a step's end.  Small kernel: 2, 4 and 8 took 139, 129 and 133 us for a
+// layer of 8 experts of 14336 x 4096 without escapes and one token.  Large: units
+// of 8, 16 and 32 tiles took 550, 528 and 533 us for 64 tokens.
+constexpr uint32_t kRangeSmall = 4, kRangeLarge = moe::kUnitTiles / stage::kNT;
 
 struct MoePlan {
     bool small, local;
@@ -1661,9 +1709,13 @@ MoePlan plan(const MoeCall &c) {
     MoePlan pl = {};
     const uint64_t slots = static_cast<uint64_t>(c.tokens) * c.top_k;
     const uint64_t H = c.up->cols, F = c.down->cols;
-    // few pairs an expert on average (one with more than eight is read once
-    // for every eight), or many
-    pl.small = slots <= 8ull * c.experts || c.tokens <= 8;
+    // by the products' multiply-adds, which is what the mma.sync kernel is slow
+    // at; the other one costs 10 to 20 us more to begin with.  Here and there, us:
+    // 8 experts of 14336 x 4096, top 2: 4 tokens (1.4e9) 373 and 364, 8 tokens
+    // (2.8e9) 437 and 420, 64 tokens 1251 and 515; 32 of 1408 x 2176, top 4: 48
+    // tokens (1.8e9) 170 and 186, 64 tokens (2.4e9) 208 and 187; 64 of 1024 x
+    // 2048, top 8: 16 tokens (0.8e9) 165 and 169, 64 tokens (3.2e9) 245 and 192
+    pl.small = slots * 3 * H * F <= 1ull << 31;
     pl.seg = pl.small ? moe::kSegSmall : moe::kSegLarge;
     pl.range = pl.small ? kRangeSmall : kRangeLarge;
     if (pl.small) {
