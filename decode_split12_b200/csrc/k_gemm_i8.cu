@@ -5,9 +5,8 @@
 //
 // x: M x K int8, w: N x K int8, sums in int32 (exact for K < 2^17), y BF16 or
 // FP32, rounded once.  Computed as Y^T = W * X^T, as the fused GEMM: rows of W
-// are the tensor core's M and up to 256 tokens its N, so one kernel serves a
-// single token (N = 16: bound by reading W) and prompts (bound by the tensor
-// cores).
+// are the tensor core's M and up to 256 tokens its N.  A few tokens (eight, and
+// little work) take a kernel of dot products, further down.
 //
 // One CTA per SM, ten warps with fixed roles: a TMA producer (128 columns of W
 // and X a stage, 128-byte swizzle), the MMA issuer (four tcgen05.mma.kind::i8
@@ -28,6 +27,13 @@
 // CTA that holds a part of a tile writes its sums to the workspace; the last
 // to arrive adds the others' to its own, scales and stores.  Integer sums do
 // not depend on their order.
+//
+// Measured (us; bytes against a measured copy's 6.53 TB/s, operations against 4.5
+// POP/s nominal): 1 token of 4096 x 14336 11.3 (0.79 of the bytes), of 28672 x 8192
+// 37 (0.97); 64 tokens of 28672 x 8192 47 (0.77); 256 tokens 61 (0.63; the
+// tensor cores' 27 us and the bytes' 39 do not quite overlap); 4096 tokens of
+// 14336 x 4096 170 (2.8 POP/s, 0.63 of the operations; cuBLAS's integer product
+// 158).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -557,6 +563,93 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
     }
 }
 
+// ---------------------------------------------------------------------------
+// A few tokens: no tensor cores, whose product starts late and is joined from
+// parts.  A group of `split` warps takes four rows of W, each thread 16 bytes of
+// them at a time, so that much of W is on its way at once; four products a dp4a,
+// sums across the group at the end.
+
+constexpr int kDotThreads = 256, kDotRows = 4;
+
+struct DotParams {
+    const int8_t *x, *w;
+    const float *x_scale, *w_scale;
+    void *y;
+    long long N;
+    int y_f32, M, K;
+    int split;  // warps to a group of rows: 1, 2, 4 or 8
+};
+
+__device__ __forceinline__ int dot16(const int4 &a, const int4 &b, int sum) {
+    return __dp4a(a.w, b.w, __dp4a(a.z, b.z, __dp4a(a.y, b.y, __dp4a(a.x, b.x, sum))));
+}
+
+// MT tokens (the last ones may not be there).
+template <int MT>
+__global__ void __launch_bounds__(kDotThreads, 2) dot_i8_kernel(const __grid_constant__ DotParams p) {
+    constexpr int kDotWarps = kDotThreads / 32, kBatch = MT <= 2 ? 4 : 2;
+    __shared__ int part[kDotWarps][kDotRows * MT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = 32 * p.split, t = threadIdx.x % threads;
+    const long long n0 = (static_cast<long long>(blockIdx.x) * (kDotWarps / p.split) + warp / p.split) * kDotRows;
+    const int8_t *row[kDotRows];
+#pragma unroll
+    for (int r = 0; r < kDotRows; ++r)  // (rows past the last are the last, and not stored)
+        row[r] = p.w + min(n0 + r, p.N - 1) * p.K;
+    int sum[kDotRows][MT];
+#pragma unroll
+    for (int r = 0; r < kDotRows; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) sum[r][m] = 0;
+    grid_launch_dependents();
+    grid_dependency_wait();  // x, w and y may belong to earlier kernels
+    for (int k0 = t * 16; k0 < p.K; k0 += kBatch * threads * 16) {
+        int4 wv[kBatch][kDotRows];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int r = 0; r < kDotRows; ++r) {
+                const int k = k0 + b * threads * 16;
+                wv[b][r] = make_int4(0, 0, 0, 0);
+                if (k < p.K) wv[b][r] = __ldcs(reinterpret_cast<const int4 *>(row[r] + k));
+            }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int k = k0 + b * threads * 16;
+            if (k < p.K) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int4 xv = __ldg(reinterpret_cast<const int4 *>(
+                        p.x + static_cast<size_t>(min(m, p.M - 1)) * p.K + k));
+#pragma unroll
+                    for (int r = 0; r < kDotRows; ++r) sum[r][m] = dot16(wv[b][r], xv, sum[r][m]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kDotRows; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int s = __reduce_add_sync(0xFFFFFFFFu, sum[r][m]);
+            if (lane == 0) part[warp][r * MT + m] = s;
+        }
+    __syncthreads();
+    if (t < kDotRows * MT) {
+        const int r = t / MT, m = t - r * MT;
+        const long long n = n0 + r;
+        if (n < p.N && m < p.M) {
+            int s = 0;
+            for (int i = 0; i < p.split; ++i) s += part[warp + i][t];
+            const float v = static_cast<float>(s) * __ldg(p.x_scale + m) * __ldg(p.w_scale + n);
+            const size_t at = static_cast<size_t>(m) * p.N + n;
+            if (p.y_f32)
+                static_cast<float *>(p.y)[at] = v;
+            else
+                static_cast<uint16_t *>(p.y)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        }
+    }
+}
+
 }  // namespace gemm8
 
 // ---------------------------------------------------------------------------
@@ -565,7 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_i8_kernel(const __grid_const
 namespace {
 
 constexpr uint32_t kSmemLimit = 227 * 1024;
-constexpr int kPairTokens = 128;  // more tokens than this: two CTAs a product
+constexpr int kDotTokens = 8;
+// More tokens than this: two CTAs a product (14336 x 4096, one and two, us: 96
+// tokens 15.6 and 16.5, 128 16.0 and 17.1, 256 20.2 and 18.9, 512 36 and 29, 4096
+// 186 and 175).
+constexpr int kPairTokens = 128;
 
 struct Plan8 {
     int cg, tokens, tiles_m;
@@ -619,6 +716,21 @@ int run8(const gemm8::Params &p, int workers, uint32_t smem, cudaStream_t stream
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? S12_OK : S12_ERR_CUDA;
 }
 
+template <int MT>
+int run_dot(const gemm8::DotParams &p, cudaStream_t stream) {
+    const long long rows = gemm8::kDotThreads / 32 / p.split * gemm8::kDotRows;  // of a block
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.N + rows - 1) / rows));
+    cfg.blockDim = dim3(gemm8::kDotThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gemm8::dot_i8_kernel<MT>, p) == cudaSuccess ? S12_OK : S12_ERR_CUDA;
+}
+
 }  // namespace
 
 size_t gemm_i8_ws_bytes(int64_t M) {
@@ -634,6 +746,24 @@ int launch_gemm_i8(const Gemm8Call &c, void *ws, size_t ws_bytes, cudaStream_t s
     if (sms > S12_WS_HEAD / 4) return S12_ERR_DEVICE;
     const Plan8 pl = plan8(c.M, sms);
     if (ws_bytes < pl.cnt_bytes + pl.part_bytes) return S12_ERR_CAPACITY;
+    // The dot products against the tensor cores, us: 1 token 14336 x 4096 12.1 and
+    // 14.7, 2 tokens 28672 x 8192 39.7 and 43.7, 3 tokens 14336 x 4096 14.7 both, 8
+    // tokens 4096 x 4096 6.6 and 11.0, 14336 x 4096 18.9 and 14.6.
+    if (c.M <= 2 || (c.M <= kDotTokens && static_cast<unsigned long long>(c.M) * c.N * c.K <= 3ull << 26)) {
+        gemm8::DotParams d = {c.x, c.w, c.x_scale, c.w_scale, c.y, c.N, c.y_type == S12_TYPE_F32,
+                              static_cast<int>(c.M), static_cast<int>(c.K), 1};
+        // eight warps an SM and rows that are not too long for one (one token, us,
+        // by 1, 2, 4 and 8 warps a group of rows: 4096 x 14336 14.2 11.3 12.4 12.9;
+        // 14336 x 4096 12.1 12.5 14.6 23.3; 28672 x 8192 40.7 37.2 37.9 49.8;
+        // 1024 x 4096 3.7 2.7 2.2 2.1)
+        while (d.split < gemm8::kDotThreads / 32 &&
+               ((c.N + 3) / 4 * d.split < 8 * sms || c.K > 7168ll * d.split))
+            d.split *= 2;
+        if (c.M == 1) return run_dot<1>(d, stream);
+        if (c.M == 2) return run_dot<2>(d, stream);
+        if (c.M <= 4) return run_dot<4>(d, stream);
+        return run_dot<8>(d, stream);
+    }
     gemm8::Params p = {};
     if (make_tmap_u8_2d(&p.tm_w, c.w, c.K, c.N, c.K, gemm8::kChunk, gemm8::kRows, 128) != S12_OK ||
         make_tmap_u8_2d(&p.tm_x, c.x, c.K, c.M, c.K, gemm8::kChunk, pl.tokens / pl.cg, 128) != S12_OK)
