@@ -341,7 +341,7 @@ __device__ __forceinline__ void epilogue(const Params &p, const Layout &L, const
     const long long n = (w.tile / p.tiles_m * CG + blockIdx.x % CG) * kRows + row, m0 = w.tile % p.tiles_m * p.tokens;
     const int m_here = static_cast<int>(min(static_cast<long long>(p.tokens), p.M - m0));
     const bool live = n < p.N;
-    const float sw = live ? __ldg(p.w_scale + n) : 0.f;
+    const float sw = live ? p.w_scale[n] : 0.f;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     int first = 0, last = 0;
     bool store = true;
@@ -368,7 +368,7 @@ __device__ __forceinline__ void epilogue(const Params &p, const Layout &L, const
     }
     if (store) {
         auto token_scale = [&](int c) {
-            return c + (lane & 15) < m_here ? __ldg(p.x_scale + m0 + c + (lane & 15)) : 0.f;
+            return c + (lane & 15) < m_here ? p.x_scale[m0 + c + (lane & 15)] : 0.f;
         };
         float sx = token_scale(16 * odd);
         for (int c = 16 * odd; c < m_here; c += 32) {
@@ -601,7 +601,8 @@ __global__ void __launch_bounds__(kDotThreads, 2) dot_i8_kernel(const __grid_con
 #pragma unroll
         for (int m = 0; m < MT; ++m) sum[r][m] = 0;
     grid_launch_dependents();
-    grid_dependency_wait();  // x, w and y may belong to earlier kernels
+    // x, w and y may belong to earlier kernels (hence no loads as constants here)
+    grid_dependency_wait();
     for (int k0 = t * 16; k0 < p.K; k0 += kBatch * threads * 16) {
         int4 wv[kBatch][kDotRows];
 #pragma unroll
@@ -618,8 +619,8 @@ __global__ void __launch_bounds__(kDotThreads, 2) dot_i8_kernel(const __grid_con
             if (k < p.K) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    const int4 xv = __ldg(reinterpret_cast<const int4 *>(
-                        p.x + static_cast<size_t>(min(m, p.M - 1)) * p.K + k));
+                    const int4 xv =
+                        *reinterpret_cast<const int4 *>(p.x + static_cast<size_t>(min(m, p.M - 1)) * p.K + k);
 #pragma unroll
                     for (int r = 0; r < kDotRows; ++r) sum[r][m] = dot16(wv[b][r], xv, sum[r][m]);
                 }
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kDotThreads, 2) dot_i8_kernel(const __grid_con
         if (n < p.N && m < p.M) {
             int s = 0;
             for (int i = 0; i < p.split; ++i) s += part[warp + i][t];
-            const float v = static_cast<float>(s) * __ldg(p.x_scale + m) * __ldg(p.w_scale + n);
+            const float v = static_cast<float>(s) * p.x_scale[m] * p.w_scale[n];
             const size_t at = static_cast<size_t>(m) * p.N + n;
             if (p.y_f32)
                 static_cast<float *>(p.y)[at] = v;

@@ -431,8 +431,8 @@ size_t s12_moe_ws_bytes(const s12_view *gate_up, const s12_view *down, int exper
  * NaN weights and a NaN y; other tokens are not affected.
  * With err_flag given, the escape counts of tile rows with escapes are
  * checked against their spans and bases above 241 are flagged.
- * The kernel is a cooperative launch of one block per SM that meets twice; a
- * bounded wait that gives up sets S12_FLAG_TIMEOUT (y is then not valid) and
+ * The kernel is a cooperative launch of one block per SM, whose blocks meet
+ * between the steps; a bounded wait that gives up sets S12_FLAG_TIMEOUT (y is then not valid) and
  * leaves the workspace ready for the next call. */
 int s12_moe(const s12_view *gate_up, const s12_view *down, int experts, const uint16_t *x, int tokens,
             const uint16_t *router, int top_k, int renorm, void *y, int y_type, int32_t *ids, float *weights,
@@ -503,8 +503,9 @@ size_t s12_gemm_i8_ws_bytes(int64_t M);
 /* Follows: [W] opening comparison of lossless weights with 8-bit ones (Q8_0):
  * the 8-bit product that the lossless one is compared with; its scales per
  * token and output channel, and the kernel, are this library's own.
- * y[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] * w[n][k], on the tensor
- * cores with exact int32 sums.
+ * y[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] * w[n][k], with exact
+ * int32 sums: on the tensor cores, or for a few tokens as dot products, with
+ * the same values.
  *   x: device int8, M x K row-major, x_scale: device FP32, M values (of
  *      s12_quant_i8 or s12_rmsnorm).
  *   w: device int8, N x K row-major, w_scale: device FP32, N values.
