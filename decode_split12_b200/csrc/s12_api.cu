@@ -429,8 +429,8 @@ int moe_shapes(const MoeCall &c) {
         c.top_k < 1 || c.top_k > S12_MOE_MAX_TOP_K)
         return S12_ERR_SHAPE;
     const uint64_t E = static_cast<uint64_t>(c.experts), H = c.up->cols, F = c.down->cols;
-    if (H > 0x3FFFFFFFull || F > 0x3FFFFFFFull || c.up->rows > 0x7FFFFFFFull || c.down->rows > 0x7FFFFFFFull)
-        return S12_ERR_SHAPE;
+    if (H > S12_MOE_MAX_COLS || F > S12_MOE_MAX_COLS) return S12_ERR_SHAPE;
+    if (c.up->rows > 0x7FFFFFFFull || c.down->rows > 0x7FFFFFFFull) return S12_ERR_SHAPE;
     return c.up->rows == E * 2 * F && c.down->rows == E * H ? S12_OK : S12_ERR_SHAPE;
 }
 

@@ -97,6 +97,7 @@ extern "C" {
 #define S12_MOE_MAX_TOKENS 64   /* tokens of one s12_moe call */
 #define S12_MOE_MAX_TOP_K 8     /* experts a token is sent to */
 #define S12_MOE_MAX_EXPERTS 256
+#define S12_MOE_MAX_COLS 4194304 /* columns of either container of s12_moe */
 
 /* ---- value types of the calls that take more than one ---- */
 #define S12_TYPE_BF16 0
@@ -407,8 +408,8 @@ size_t s12_moe_ws_bytes(const s12_view *gate_up, const s12_view *down, int exper
  *            as in s12_gemv_swiglu (the binding's interleave_gate_up, applied
  *            to the stacked matrices, builds it).
  *   down:    ONE container of experts * H rows and F columns.  Shapes that do
- *            not fit together give S12_ERR_SHAPE.  Both are version 1, or
- *            both version 2.
+ *            not fit together, and H or F above S12_MOE_MAX_COLS, give
+ *            S12_ERR_SHAPE.  Both are version 1, or both version 2.
  *   x:       device BF16, tokens x H; 0 <= tokens <= S12_MOE_MAX_TOKENS (0
  *            does nothing).
  *   router:  device BF16, experts x H; 1 <= experts <= S12_MOE_MAX_EXPERTS,

@@ -126,3 +126,17 @@ def test_gemm_i8_refusals(s12):
     assert call(y=C.c_void_p(0x100002), yt=1) == L
     assert call(M=0, x=None, y=None) == s12.S12_OK and call(N=0, w=None, ws=None) == s12.S12_OK
     assert lib.s12_gemm_i8_ws_bytes(-1) == 0 and lib.s12_gemm_i8_ws_bytes(1 << 31) == 0
+
+
+def test_moe_refuses_rows_whose_places_pass_32_bits(s12):
+    """512 pairs of rows of more than 2^22 columns: their pieces would no longer count in 31 bits."""
+    lib = s12.lib()
+    most = 1 << 22
+    for H, F in ((most + 128, 128), (128, most + 128)):
+        u, d = views(s12, E=1, H=H, F=F)
+        assert lib.s12_moe_ws_bytes(C.byref(u), C.byref(d), 1, 1, 1) == 0
+        assert lib.s12_moe(C.byref(u), C.byref(d), 1, OK_PTR, 1, OK_PTR, 1, 1, OK_PTR, 0, None, None, OK_PTR, 1 << 40,
+                           None, None) == s12.S12_ERR_SHAPE
+    u, d = views(s12, E=1, H=most, F=128)
+    assert lib.s12_moe(C.byref(u), C.byref(d), 1, OK_PTR, 0, OK_PTR, 1, 1, OK_PTR, 0, None, None, OK_PTR, 0, None,
+                       None) == s12.S12_OK
