@@ -1090,7 +1090,7 @@ struct Unit {
     int j, n;  // first tile; tiles (0: no more units)
 };
 
-// The CTA's unit `ord`: 1, or 0 when it is not known yet.
+// The CTA's unit `ord`; false when it is not known yet.
 template <int PH>
 __device__ __forceinline__ bool peek(const Params &p, const LargeShared *sm, uint32_t ord, Unit &u) {
     const Step &st = sm->step[PH - 1];
@@ -1132,7 +1132,8 @@ __device__ __forceinline__ bool lost(const Params &p, LargeShared *sm) {
     return false;
 }
 
-// Bytes of the x of n pairs in a stage (one plane), rows rounded up for the product.
+// Pairs of a product (a multiple of 16) for n that there are; the rest are whatever
+// shared memory holds, and their sums are not read.
 __device__ __forceinline__ uint32_t product_pairs(uint32_t n) { return (n + 15u) & ~15u; }
 
 struct Stages {
