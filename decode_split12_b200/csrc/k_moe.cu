@@ -112,7 +112,6 @@ struct __align__(64) Params {
 };
 
 struct Shared {
-    unsigned long long bars[kWarps * kStages];
     float weight[kMaxSlots];
     int16_t expert[kMaxSlots];  // of each (token, slot), -1 for none
     uint16_t token[kMaxSlots];  // of each pair of the list: the (token, slot) pairs by expert
@@ -555,6 +554,7 @@ struct Step {
 };
 
 struct SmallShared {
+    unsigned long long bars[kWarps * kStages];
     Shared s;
     Step step[2];
 };
@@ -957,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_small_kernel(const __grid_con
     SmallShared *sm = reinterpret_cast<SmallShared *>(base + kRingBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Ring rg;
-    rg.bars = smem_addr(sm->s.bars) + static_cast<uint32_t>(warp) * kStages * 8u;
+    rg.bars = smem_addr(sm->bars) + static_cast<uint32_t>(warp) * kStages * 8u;
     rg.base = smem_addr(base) + static_cast<uint32_t>(warp) * kStages * kStageBytes;
     rg.issued = rg.consumed = 0;
     if (lane == 0) {
@@ -1062,7 +1062,7 @@ constexpr int kDecodeWarps = kGroups * kGroupWarps, kMetaWarps = 2;
 constexpr int kLargeThreads = 32 * (2 + kDecodeWarps + kMetaWarps);
 constexpr int kUnitTiles = 16;   // tiles of a unit at most
 constexpr int kAhead = 3;        // units that a CTA knows in advance
-constexpr int kUnits = 32;       // the queue: no warp is more than 16 tiles behind the copies
+constexpr int kUnits = 24;       // the queue: no warp is more than 16 tiles behind the copies
 constexpr int kMaxRing = 8;      // stages
 constexpr int kBlockRows = 128;
 constexpr uint32_t kTileRaw = kBlockRows * kTile, kTileBytes = kTileRaw + kTileRaw / 2;
@@ -1132,9 +1132,16 @@ __device__ __forceinline__ bool lost(const Params &p, LargeShared *sm) {
     return false;
 }
 
-// Pairs of a product (a multiple of 16) for n that there are; the rest are whatever
-// shared memory holds, and their sums are not read.
-__device__ __forceinline__ uint32_t product_pairs(uint32_t n) { return (n + 15u) & ~15u; }
+// Pairs of a product for n that there are (its columns, two for each pair of h,
+// are a multiple of 16); the rest are whatever shared memory holds, and their sums
+// are not read.  Stages are as long as the largest segment needs, and their number
+// tells: with h in eights, 33 to 40 pairs leave four stages instead of three (64
+// tokens: 525 us against 555).
+template <int PH>
+__device__ __forceinline__ uint32_t product_pairs(uint32_t n) {
+    constexpr uint32_t kUp = 16 / PH - 1;
+    return (n + kUp) & ~kUp;
+}
 
 struct Stages {
     uint32_t base, bytes, n;
@@ -1144,7 +1151,7 @@ template <int PH>
 __device__ __forceinline__ Stages stages_of(const Params &p, const LargeShared *sm, uint32_t base) {
     Stages s;
     s.base = base;
-    s.bytes = kTileBytes + product_pairs(static_cast<uint32_t>(sm->s.most)) * 256u * PH;  // (h: two planes)
+    s.bytes = kTileBytes + product_pairs<PH>(static_cast<uint32_t>(sm->s.most)) * 256u * PH;  // (h: two planes)
     s.n = min(static_cast<uint32_t>(kMaxRing), p.pool / s.bytes);
     return s;
 }
@@ -1194,7 +1201,7 @@ __device__ __forceinline__ void copy_step(const Params &p, LargeShared *sm, uint
         const Unit u = unit_at<PH>(p, sm, ord);
         if (u.n == 0) break;
         const uint32_t claimed = atomicAdd(p.sync + (PH == 1 ? kNext1 : kNext2), 1u) + kAhead * gridDim.x;
-        const uint32_t row = row_of<PH>(p, sm, u), n = sm->s.seg_n[u.seg], atom = product_pairs(n) * 128u;
+        const uint32_t row = row_of<PH>(p, sm, u), n = sm->s.seg_n[u.seg], atom = product_pairs<PH>(n) * 128u;
         const size_t off = sm->s.seg_first[u.seg] * line;
         for (int t = 0; t < u.n; ++t) {
             ok = mbar_wait_s(smem_addr(&sm->empty[PH - 1][slot]), parity);
@@ -1278,7 +1285,7 @@ __device__ __forceinline__ void multiply_step(const Params &p, LargeShared *sm, 
         const Unit u = unit_at<PH>(p, sm, ord);
         const uint32_t tiles = uniform(static_cast<uint32_t>(u.n));
         if (tiles == 0) break;
-        const uint32_t n = PH * uniform(product_pairs(sm->s.seg_n[u.seg])), idesc = product_desc(n);
+        const uint32_t n = PH * uniform(product_pairs<PH>(sm->s.seg_n[u.seg])), idesc = product_desc(n);
         const uint32_t sums = tm + (ord & 1u) * kSumCols;
         ok = mbar_wait_s(smem_addr(&sm->stored[PH - 1][ord & 1u]), ((ord >> 1) & 1u) ^ 1u);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -1543,7 +1550,7 @@ __device__ __forceinline__ void decode_step(const Params &p, LargeShared *sm, ui
                 uint32_t v[PH][2][4];  // (of the high and the low part of h)
 #pragma unroll
                 for (int i = 0; i < 2 * PH; ++i)
-                    tc::tmem_ld4(sums + (i >> 1) * product_pairs(pairs) + c + 4 * (i & 1), v[i >> 1][i & 1]);
+                    tc::tmem_ld4(sums + (i >> 1) * product_pairs<PH>(pairs) + c + 4 * (i & 1), v[i >> 1][i & 1]);
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -1621,7 +1628,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_large_kernel(const __gri
             if (threadIdx.x == 0) sm->step[0] = plan_step<1>(p, &sm->s, kGroupsOfBlock);
             if (threadIdx.x == 32) sm->step[1] = plan_step<2>(p, &sm->s, kGroupsOfBlock);
             if (threadIdx.x >= 64 && threadIdx.x < 64 + 2 * kUnits) {
-                const uint32_t k = threadIdx.x % kUnits;
+                const uint32_t k = (threadIdx.x - 64) % kUnits;
                 sm->queue[(threadIdx.x - 64) / kUnits][k] =
                     k < kAhead ? (static_cast<unsigned long long>(k) << 32) | (blockIdx.x + k * gridDim.x) : ~0ull;
             }
