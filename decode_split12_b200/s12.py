@@ -443,9 +443,9 @@ def _here(t: torch.Tensor | None, dev: int):
     return t.data_ptr()
 
 
-def _raw_stream(stream, dev: int):
-    if stream is not None:
-        return stream.cuda_stream
+def _raw_stream(dev: int):
+    """The current stream.  A call with a stream makes it the current one, so
+    that what it allocates is cleared, written and given back on it."""
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
@@ -491,6 +491,9 @@ def s12_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
     itself where none is given.  Returns (y, q, scale, residual_out): y, the
     norm as BF16 bits, where `bf16`; q (int8) and scale (FP32, one a row)
     where `int8`; None for what was not asked for."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return s12_rmsnorm(x, weight, eps, residual, residual_out, bf16, int8, y, q, scale)
     if not (bf16 or int8):
         raise ValueError("nothing to compute: neither bf16 nor int8")
     shape = x.shape
@@ -516,7 +519,7 @@ def s12_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
     dev = torch.cuda.current_device()
     rc = _lib().s12_rmsnorm(_here(x, dev), _value_type(x), _here(residual, dev), _here(residual_out, dev), rt,
                             _here(weight, dev), rows, cols, eps, _here(y, dev), _here(q, dev), _here(scale, dev),
-                            _raw_stream(stream, dev))
+                            _raw_stream(dev))
     if rc:
         raise S12Error(rc, "s12_rmsnorm")
     return y, q, scale, residual_out
@@ -525,6 +528,9 @@ def s12_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
 def s12_quant_i8(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
     """(q, scale): the rows of x (BF16 or FP32, along its last dimension) as
     int8 with one FP32 scale a row."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return s12_quant_i8(x, q, scale)
     shape = x.shape
     cols = shape[-1]
     rows = x.numel() // cols if cols else 0
@@ -532,7 +538,7 @@ def s12_quant_i8(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Te
     scale = _or_empty(scale, x, shape[:-1], torch.float32, (torch.float32,), "scale")
     dev = torch.cuda.current_device()
     rc = _lib().s12_quant_i8(_here(x, dev), _value_type(x), rows, cols, _here(q, dev), _here(scale, dev),
-                             _raw_stream(stream, dev))
+                             _raw_stream(dev))
     if rc:
         raise S12Error(rc, "s12_quant_i8")
     return q, scale
@@ -553,6 +559,9 @@ def s12_gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
                 stream=None, f32: bool = False) -> torch.Tensor:
     """y = x_scale[m] * w_scale[n] * (x w^T) of int8 x (M, K) and w (N, K), as
     BF16 bits (or FP32 where `f32`, or in the type of the y that is given)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return s12_gemm_i8(x, x_scale, w, w_scale, y, ws, err_flag, f32=f32)
     M, K = x.shape
     N = w.shape[0]
     if x.dtype is not torch.int8:
@@ -566,7 +575,7 @@ def s12_gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     dev = torch.cuda.current_device()
     rc = _lib().s12_gemm_i8(_here(x, dev), _here(x_scale, dev), _here(w, dev), _here(w_scale, dev), M, N, K,
                             _here(y, dev), _value_type(y), _here(ws, dev), ws.numel() * ws.element_size(),
-                            _here(err_flag, dev), _raw_stream(stream, dev))
+                            _here(err_flag, dev), _raw_stream(dev))
     if rc:
         raise S12Error(rc, "s12_gemm_i8")
     return y
@@ -598,6 +607,9 @@ def s12_moe(gate_up: View, down: View, experts: int, x: torch.Tensor, router: to
     experts (int32) and their weights (FP32), tokens x top_k.  gate_up is the
     container of interleave_gate_up(gate, up) of the experts' matrices
     stacked along their rows, down that of the stacked down matrices."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return s12_moe(gate_up, down, experts, x, router, top_k, renorm, y, ids, weights, ws, err_flag, f32=f32)
     y = _moe_io(down, x, experts, y, f32)
     T = x.shape[0]
     _expect(router, (experts, x.shape[1]), _BITS16, "router")
@@ -609,7 +621,7 @@ def s12_moe(gate_up: View, down: View, experts: int, x: torch.Tensor, router: to
     rc = _lib().s12_moe(C.byref(gate_up), C.byref(down), experts, _here(x, dev), T, _here(router, dev), top_k,
                         int(renorm), _here(y, dev), _value_type(y), _here(ids, dev), _here(weights, dev),
                         _here(ws, dev), ws.numel() * ws.element_size(), _here(err_flag, dev),
-                        _raw_stream(stream, dev))
+                        _raw_stream(dev))
     if rc:
         raise S12Error(rc, "s12_moe")
     return y, ids, weights
@@ -620,6 +632,9 @@ def s12_moe_routed(gate_up: View, down: View, experts: int, x: torch.Tensor, ids
                    err_flag: torch.Tensor | None = None, stream=None, f32: bool = False) -> torch.Tensor:
     """s12_moe with the routing given (ids int32 and weights FP32, tokens x
     top_k; an id outside [0, experts) leaves its slot out): y."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return s12_moe_routed(gate_up, down, experts, x, ids, weights, y, ws, err_flag, f32=f32)
     y = _moe_io(down, x, experts, y, f32)
     T = x.shape[0]
     if ids.dim() != 2:
@@ -632,7 +647,7 @@ def s12_moe_routed(gate_up: View, down: View, experts: int, x: torch.Tensor, ids
     dev = torch.cuda.current_device()
     rc = _lib().s12_moe_routed(C.byref(gate_up), C.byref(down), experts, _here(x, dev), T, _here(ids, dev),
                                _here(weights, dev), top_k, _here(y, dev), _value_type(y), _here(ws, dev),
-                               ws.numel() * ws.element_size(), _here(err_flag, dev), _raw_stream(stream, dev))
+                               ws.numel() * ws.element_size(), _here(err_flag, dev), _raw_stream(dev))
     if rc:
         raise S12Error(rc, "s12_moe_routed")
     return y
