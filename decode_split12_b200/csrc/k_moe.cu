@@ -212,18 +212,17 @@ __device__ __forceinline__ void pack_sorted(const Params &p, const Shared *sm, i
     }
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &a, float (&v)[8]) {
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
+// Value c of eight.
+__device__ __forceinline__ double value_of(const uint4 &a, int c) {
+    const uint32_t u = c < 4 ? (c < 2 ? a.x : a.y) : (c < 6 ? a.z : a.w);
+    return static_cast<double>(__uint_as_float(c & 1 ? u & 0xFFFF0000u : u << 16));
 }
 
-// Scores of TT tokens and TE experts to a warp.  The products of BF16 values
-// are exact in FP32; eight of them are added in FP32, the rest in 64 bits,
-// because the choice of experts hangs on the order of the scores.
+// Scores of TT tokens and TE experts to a warp, in 64 bits throughout, because
+// the choice of experts hangs on the order of the scores: a product of BF16
+// values is exact there, and none is too large or too small.  What it costs are
+// the conversions (12 a cycle and SM; products 60), and code: eight loads in
+// flight instead of four, with their 64 conversions each, took 1 us longer.
 template <int TT, int TE>
 __device__ __forceinline__ void score(const Params &p, double *scores, int u0, int step) {
     const int lane = threadIdx.x & 31;
@@ -235,7 +234,7 @@ __device__ __forceinline__ void score(const Params &p, double *scores, int u0, i
         for (int i = 0; i < TT; ++i)
 #pragma unroll
             for (int j = 0; j < TE; ++j) acc[i][j] = 0.0;
-        constexpr int kBatch = TT == 1 ? 8 : 1;  // loads in flight
+        constexpr int kBatch = TT == 1 ? 4 : 1;  // loads in flight
         for (int k0 = lane * 8; k0 < p.H; k0 += 256 * kBatch) {
             uint4 xr[kBatch][TT], rr[kBatch][TE];
 #pragma unroll
@@ -256,19 +255,17 @@ __device__ __forceinline__ void score(const Params &p, double *scores, int u0, i
             }
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-                float xv[TT][8];
+                if (k0 - lane * 8 + 256 * b >= p.H) break;
 #pragma unroll
-                for (int i = 0; i < TT; ++i) unpack8(xr[b][i], xv[i]);
+                for (int c = 0; c < 8; ++c) {
+                    double xv[TT];
 #pragma unroll
-                for (int j = 0; j < TE; ++j) {
-                    float rv[8];
-                    unpack8(rr[b][j], rv);
+                    for (int i = 0; i < TT; ++i) xv[i] = value_of(xr[b][i], c);
 #pragma unroll
-                    for (int i = 0; i < TT; ++i) {
-                        float s = xv[i][0] * rv[0];
+                    for (int j = 0; j < TE; ++j) {
+                        const double rv = value_of(rr[b][j], c);
 #pragma unroll
-                        for (int c = 1; c < 8; ++c) s = fmaf(xv[i][c], rv[c], s);
-                        acc[i][j] += static_cast<double>(s);
+                        for (int i = 0; i < TT; ++i) acc[i][j] = fma(xv[i], rv, acc[i][j]);
                     }
                 }
             }
@@ -1730,8 +1727,11 @@ MoePlan plan(const MoeCall &c) {
         const uint32_t fixed = 1024 + moe::kRingBytes + align_up(sizeof(moe::SmallShared), 16);
         const uint64_t x_bytes = 2ull * c.tokens * H;
         // little enough for every CTA to do alone: less time than a meeting of the grid
+        // (one token, alone and by the grid, us: 8 experts of 4096 columns 48.1 and
+        // 51.2, of 1024 43.9 and 44.1, 32 of 1024 46.1 and 45.2, 16 of 4096 50.6 and 50.8,
+        // 64 of 1024 48.5 and 44.6; 8 tokens, 16 experts of 1024 49.5 and 39.9)
         pl.local = fixed + x_bytes <= kSmemLimit && c.tokens * c.experts <= 512 &&
-                   (c.ids_in || static_cast<uint64_t>(c.tokens) * c.experts * H <= (1u << 18));
+                   (c.ids_in || static_cast<uint64_t>(c.tokens) * c.experts * H <= (1u << 15));
         pl.smem = fixed + static_cast<uint32_t>(pl.local ? x_bytes : 0);
     } else {
         const uint32_t fixed = 1024 + align_up(sizeof(moe::LargeShared), 1024);

@@ -425,7 +425,8 @@ size_t s12_moe_ws_bytes(const s12_view *gate_up, const s12_view *down, int exper
  *            any shapes for which it is large enough may use it one after
  *            the other, captured in a graph or not, s12_gemm_i8's too.
  *            Calls that may run at the same time need different workspaces.
- * The scores are sums in 64 bits.  The products accumulate in FP32 and the
+ * The scores are sums in 64 bits, of products that are exact.  The products
+ * with the experts' weights accumulate in FP32 and the
  * hidden values are held as the sum of two BF16 values, so y is within 1e-3
  * of the sum of its terms' magnitudes before its own rounding, as in
  * s12_gemv; repeated calls give identical y.  A token with a NaN score gets
