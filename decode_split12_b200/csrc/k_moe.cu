@@ -284,8 +284,9 @@ __device__ __forceinline__ void score(const Params &p, double *scores, int u0, i
 }
 
 // The experts and weights of token t, by one warp: the top_k largest scores,
-// the lower index first where two are equal (a NaN counts as -infinity, and
-// makes the token's weights NaN).
+// the lower index first where two are equal.  A NaN among the scores counts as
+// -infinity in their order and makes all the token's weights NaN, also those of
+// experts whose own scores are numbers.
 __device__ __forceinline__ void select_experts(const Params &p, Shared *sm, const double *scores, int t) {
     constexpr int kPer = S12_MOE_MAX_EXPERTS / 32;
     const int lane = threadIdx.x & 31;
@@ -294,6 +295,7 @@ __device__ __forceinline__ void select_experts(const Params &p, Shared *sm, cons
     // scores as integers of the same order, 0 for an expert that is chosen or not there
     unsigned long long key[kPer];
     double v[kPer];
+    bool nan = false;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         key[i] = 0;
@@ -302,11 +304,15 @@ __device__ __forceinline__ void select_experts(const Params &p, Shared *sm, cons
         const int e = lane + 32 * i;
         if (e < p.experts) {
             v[i] = row[e];
-            if (v[i] != v[i]) v[i] = low;
+            if (v[i] != v[i]) {
+                v[i] = low;
+                nan = true;
+            }
             const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v[i] + 0.0));
             key[i] = b >> 63 ? ~b : b | 1ull << 63;  // (-infinity: 2^52 - 1)
         }
     }
+    nan = __any_sync(0xFFFFFFFFu, nan);
     double top = 0.0;
     float mine = 0.f;  // lane s < top_k: the weight of slot s before its division
     int chosen = -1;
@@ -345,11 +351,12 @@ __device__ __forceinline__ void select_experts(const Params &p, Shared *sm, cons
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane < p.top_k) {
         const int i = t * p.top_k + lane;
+        const float weight = nan ? __uint_as_float(0x7FC00000u) : mine / sum;
         sm->expert[i] = static_cast<int16_t>(chosen);
-        sm->weight[i] = mine / sum;
+        sm->weight[i] = weight;
         if (blockIdx.x == 0) {
             if (p.ids) p.ids[i] = chosen;
-            if (p.weights) p.weights[i] = mine / sum;
+            if (p.weights) p.weights[i] = weight;
         }
     }
 }

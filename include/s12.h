@@ -426,11 +426,12 @@ size_t s12_moe_ws_bytes(const s12_view *gate_up, const s12_view *down, int exper
  *            the other, captured in a graph or not, s12_gemm_i8's too.
  *            Calls that may run at the same time need different workspaces.
  * The scores are sums in 64 bits, of products that are exact.  The products
- * with the experts' weights accumulate in FP32 and the
- * hidden values are held as the sum of two BF16 values, so y is within 1e-3
- * of the sum of its terms' magnitudes before its own rounding, as in
- * s12_gemv; repeated calls give identical y.  A token with a NaN score gets
- * NaN weights and a NaN y; other tokens are not affected.
+ * with the experts' weights accumulate in FP32 and the hidden values are held
+ * as the sum of two BF16 values, so y is within 1e-3 of the sum of its terms'
+ * magnitudes before its own rounding, as in s12_gemv; repeated calls give
+ * identical y.  A token with a NaN among its scores, of whatever expert, gets
+ * NaN weights and a NaN y (its ids are chosen as if the NaN were -infinity);
+ * other tokens are not affected.
  * With err_flag given, the escape counts of tile rows with escapes are
  * checked against their spans and bases above 241 are flagged.
  * The kernel is a cooperative launch of one block per SM, whose blocks meet

@@ -1,5 +1,5 @@
-"""The routing of s12_moe against scores in 64 bits: orders that hang on terms which 32 bits lose, and scores
-whose products leave FP32's range.  Tolerances of y: test_gpu_moe.py."""
+"""The routing of s12_moe against scores in 64 bits: orders that hang on terms which 32 bits lose, scores whose
+products leave FP32's range, and scores that are NaN.  Tolerances of y: test_gpu_moe.py."""
 import numpy as np
 import pytest
 import torch
@@ -96,3 +96,39 @@ def test_products_outside_the_range_of_32_bits(s12, form):  # noqa: F811
     _, ids, w = s12.s12_moe(*L.views, L.E, xb.cuda(), L.router, k)
     assert np.array_equal(ids.cpu().numpy(), want)
     assert np.abs(w.cpu().numpy() - weights).max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("form", FORMS)
+def test_nan_in_one_router_row_reaches_every_token(s12, form, renorm):  # noqa: F811
+    """Every token has one score that is NaN, and top_k or more that are not: weights and y are NaN; the others'
+    order is theirs, and the NaN comes behind them."""
+    L, T, k = layer(s12, form)
+    x = L.tokens(T, 2)
+    bad = L.E // 2
+    L.router[bad, L.H - 3] = float("nan")
+    y, ids, w = s12.s12_moe(*L.views, L.E, x, L.router, k, renorm=renorm)
+    assert bool(torch.isnan(w).all()) and bool(torch.isnan(y.view(torch.bfloat16)).all())
+    score = torch.nan_to_num(x.double() @ L.router.double().T, nan=-np.inf).cpu().numpy()
+    assert np.array_equal(ids.cpu().numpy(), np.stack([np.lexsort((np.arange(L.E), -s))[:k] for s in score]))
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("form", FORMS)
+def test_infinite_router_value_reaches_the_tokens_it_meets(s12, form, renorm):  # noqa: F811
+    """One infinity in a router row: a token with 0 there has a NaN score, one above 0 a score of infinity (both make
+    its weights NaN), one below 0 minus infinity, which leaves that expert out and nothing else."""
+    L, T, k = layer(s12, form)
+    x = L.tokens(T, 3)
+    bad, c = L.E - 1, 11
+    kind = torch.arange(T, device="cuda") % 3
+    x[:, c] = torch.where(kind == 0, -1.0, torch.where(kind == 1, 0.0, 1.0)).to(torch.bfloat16)
+    L.router[bad, c] = float("inf")
+    y, ids, w = s12.s12_moe(*L.views, L.E, x, L.router, k, renorm=renorm)
+    y = y.view(torch.bfloat16)
+    assert bool(torch.isnan(w[kind > 0]).all()) and bool(torch.isnan(y[kind > 0]).all())
+    fine = kind == 0
+    want, weights = choose(L, x[fine], k, renorm)
+    assert np.array_equal(ids[fine].cpu().numpy(), want) and not bool((ids[fine] == bad).any())
+    assert np.abs(w[fine].cpu().numpy() - weights).max() <= 2.0 ** -20
+    check(y[fine].view(torch.int16), *reference(L, x[fine], want, weights))
