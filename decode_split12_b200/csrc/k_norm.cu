@@ -116,9 +116,87 @@ __device__ __forceinline__ uint32_t to_eight(float a, float b, float c, float d)
     return v;
 }
 
+// s * weight.
+template <int NV>
+__device__ __forceinline__ void weigh(const Args &a, int t, int n, float (&s)[NV][kVec]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = t + i * n;
+        if (a.w && c * kVec < a.cols) {
+            float w[kVec];
+            unpack(reinterpret_cast<const uint4 *>(a.w)[c], w);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) s[i][k] *= w[k];
+        }
+    }
+}
+
+template <int NV>
+__device__ __forceinline__ uint32_t largest(const float (&s)[NV][kVec]) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) top = max(top, __float_as_uint(s[i][k]) & 0x7FFFFFFFu);
+    return top;
+}
+
+template <int NV>
+__device__ __forceinline__ float squares(const float (&s)[NV][kVec]) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) ss = fmaf(s[i][k], s[i][k], ss);
+    return ss;
+}
+
+// The sum of a row whose squares leave FP32's range, and its products with the
+// weights: the row times 2^-by, which is exact, has its largest value or the root
+// of eps near 1.  `part`: the thread's values s where it `keeps` them, else its p;
+// it becomes p * 2^-by, f the factor and top the largest that go with it.  A row
+// of zeros or one that is not finite is left as it is (false).  A function of its
+// own, on local memory: in the row's registers it took 5 % of all rows' time, so
+// it takes 3 (4096 rows of 8192: 40.2 us without it, 41.4 with it, 42.3 inline;
+// one row of 4096 2.16, 2.20 and 2.16).
+template <class Reduce>
+__device__ __noinline__ bool rescale(float *part, int vecs, bool keeps, float mine, const uint16_t *w, int cols,
+                                     float eps, int t, int n, float &f, uint32_t &top, Reduce reduce) {
+    uint32_t big = __float_as_uint(__fsqrt_rn(mine));
+    if (keeps) {
+        big = 0u;
+        for (int i = 0; i < vecs * kVec; ++i) big = max(big, __float_as_uint(part[i]) & 0x7FFFFFFFu);
+    }
+    float ss = 0.f;
+    reduce(ss, big, 1);
+    if (big == 0u || big >= 0x7F800000u) return false;
+    const int by = max(ilogbf(__uint_as_float(big)), eps > 0.f ? ilogbf(eps) / 2 : -149);
+    ss = keeps ? 0.f : scalbnf(mine, -2 * by);
+    top = 0u;
+    for (int i = 0; i < vecs * kVec; ++i) {
+        float v = scalbnf(part[i], -by);
+        if (keeps) {
+            const int c = (t + i / kVec * n) * kVec + i % kVec;
+            ss = fmaf(v, v, ss);
+            if (w && c < cols) v *= __uint_as_float(static_cast<uint32_t>(w[c]) << 16);
+        }
+        part[i] = v;
+        top = max(top, __float_as_uint(v) & 0x7FFFFFFFu);
+    }
+    reduce(ss, top, 2);
+    f = __frsqrt_rn(ss / static_cast<float>(cols) + scalbnf(eps, -2 * by));
+    return true;
+}
+
+// A mean square (with eps) below this is not taken from FP32's squares: above it
+// what they lose (2^-150 each) is far below the sum's rounding, and p * f is
+// within 2^-130 of v where p is subnormal.
+constexpr float kLeast = 0x1p-40f, kMost = 3.4028234e38f;
+
 // One row by n threads (t = 0 .. n-1), `reduce` summing ss and taking the
-// largest top over them.  PLAIN: the quantiser (x to q and scale, nothing
-// else), which needs fewer registers.
+// largest top over them (its last argument: how often it was called before).
+// PLAIN: the quantiser (x to q and scale, nothing else), which needs fewer
+// registers.
 template <int NV, bool PLAIN, class Reduce>
 __device__ __forceinline__ void do_row(const Args &a, long long row, int t, int n, Reduce reduce) {
     const size_t row0 = static_cast<size_t>(row) * static_cast<size_t>(a.cols);
@@ -147,26 +225,31 @@ __device__ __forceinline__ void do_row(const Args &a, long long row, int t, int 
             }
         }
     }
-    float ss = 0.f;
-    uint32_t top = 0u;
+    const float mine = PLAIN ? 0.f : squares(s);
+    // A thread keeps its part of a row whose squares may leave FP32's range, before
+    // it is multiplied.  No thread's sum is more than the row's, so where the row's
+    // mean is below kLeast all of them have kept theirs.
+    float part[NV * kVec];
+    const bool keeps = !PLAIN && !(mine >= (a.eps < kLeast ? kLeast * S12_NORM_MAX_COLS : 0.f) && mine <= kMost);
+    auto put = [&]() {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = t + i * n;
-#pragma unroll
-        for (int k = 0; k < kVec && !PLAIN; ++k) ss = fmaf(s[i][k], s[i][k], ss);
-        if (!PLAIN && a.w && c * kVec < a.cols) {
-            float w[kVec];
-            unpack(reinterpret_cast<const uint4 *>(a.w)[c], w);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) s[i][k] *= w[k];
-        }
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) top = max(top, __float_as_uint(s[i][k]) & 0x7FFFFFFFu);
-    }
-    reduce(ss, top);
+        for (int i = 0; i < NV * kVec; ++i) part[i] = s[i / kVec][i % kVec];
+    };
+    if (keeps) put();
+    if (!PLAIN) weigh(a, t, n, s);
+    float ss = mine;
+    uint32_t top = largest(s);
+    reduce(ss, top, 0);
     // (a row of zeros with eps = 0 stays a row of zeros)
     const float ms = ss / static_cast<float>(a.cols) + a.eps;
-    const float f = PLAIN ? 1.f : ms == 0.f ? 0.f : __frsqrt_rn(ms);
+    float f = PLAIN ? 1.f : ms == 0.f ? 0.f : __frsqrt_rn(ms);
+    if (!PLAIN && !(ms >= kLeast && ms <= kMost)) {
+        if (!keeps) put();
+        if (rescale(part, NV, keeps, mine, a.w, a.cols, a.eps, t, n, f, top, reduce)) {
+#pragma unroll
+            for (int i = 0; i < NV * kVec; ++i) s[i / kVec][i % kVec] = part[i];
+        }
+    }
     if (!PLAIN && a.y) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -220,26 +303,26 @@ __global__ void __launch_bounds__(32 * kWarpRows) warp_kernel(const Args a) {
     const long long row = static_cast<long long>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5);
     if (row >= a.rows) return;
     grid_dependency_wait();
-    do_row<NV, PLAIN>(a, row, threadIdx.x & 31, 32, [](float &ss, uint32_t &top) { warp_reduce(ss, top); });
+    do_row<NV, PLAIN>(a, row, threadIdx.x & 31, 32, [](float &ss, uint32_t &top, int) { warp_reduce(ss, top); });
 }
 
 // One row to a block of at most THREADS threads, BLOCKS of them on an SM.
 template <int NV, bool PLAIN, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) block_kernel(const Args a) {
-    __shared__ float part[32];
-    __shared__ uint32_t tops[32];
+    __shared__ float part[3][32];
+    __shared__ uint32_t tops[3][32];
     grid_launch_dependents();
     grid_dependency_wait();
-    do_row<NV, PLAIN>(a, blockIdx.x, threadIdx.x, blockDim.x, [&](float &ss, uint32_t &top) {
+    do_row<NV, PLAIN>(a, blockIdx.x, threadIdx.x, blockDim.x, [&](float &ss, uint32_t &top, int at) {
         warp_reduce(ss, top);
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
         if (lane == 0) {
-            part[warp] = ss;
-            tops[warp] = top;
+            part[at][warp] = ss;
+            tops[at][warp] = top;
         }
         __syncthreads();
-        ss = lane < warps ? part[lane] : 0.f;
-        top = lane < warps ? tops[lane] : 0u;
+        ss = lane < warps ? part[at][lane] : 0.f;
+        top = lane < warps ? tops[at][lane] : 0u;
         warp_reduce(ss, top);
     });
 }

@@ -478,9 +478,11 @@ int s12_moe_routed(const s12_view *gate_up, const s12_view *down, int experts, c
  * any number below 2^31; rows == 0 does nothing.  eps >= 0 and finite (else
  * S12_ERR_ARG).
  * A row of zeros has scale 0 and q 0.  A row with an infinity or a NaN (or
- * one that s or s * weight overflows to) has q 0 and scale NaN, and y what
- * FP32 arithmetic gives.  The sum of squares is held in FP32: it overflows,
- * and the row's v become 0, for |s| above about 1e19.  q rounds an FP32
+ * one that s overflows to, or s * weight where the row's squares stay in
+ * FP32's range) has q 0 and scale NaN, and y what FP32 arithmetic gives.
+ * Rows whose squares leave FP32's range are scaled first, so v is right for
+ * every finite s and every eps; a v below 2^-110 may be off by 2^-130, and a
+ * scale below FP32's least value is 0.  q rounds an FP32
  * quotient: a value within 2^-22 relative of a half step may go either way.
  * The largest |q| of a finite row is 127, unless the row is all zeros. */
 int s12_rmsnorm(const void *x, int x_type, const void *residual, void *residual_out, int residual_type,
