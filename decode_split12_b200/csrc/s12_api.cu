@@ -106,42 +106,43 @@ CUtensorMapSwizzle swizzle_mode(int swizzle) {
                            : CU_TENSOR_MAP_SWIZZLE_NONE;
 }
 
+// An encoding wants a context that is current on the calling thread.  A host
+// thread that has made no CUDA call that works on a device has none yet (asking
+// for the device does not make one): it is given the device's.
+template <class Encode>
+int encode(Encode call) {
+    auto enc = encoder();
+    if (!enc) return S12_ERR_CUDA;
+    if (call(enc) == CUDA_SUCCESS) return S12_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return S12_ERR_CUDA;
+    return call(enc) == CUDA_SUCCESS ? S12_OK : S12_ERR_CUDA;
+}
+
 int encode_2d(CUtensorMap *out, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t rows,
               uint64_t row_stride, uint32_t box_inner, uint32_t box_rows, int swizzle) {
-    std::call_once(g_encode_once, [] {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    });
-    if (!g_encode_tiled) return S12_ERR_CUDA;
     const cuuint64_t dims[2] = {inner, rows};
     const cuuint64_t strides[1] = {row_stride};
     const cuuint32_t box[2] = {box_inner, box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode_tiled(out, dtype, 2, const_cast<void *>(base), dims, strides, box,
-                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                : CU_TENSOR_MAP_SWIZZLE_NONE,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? S12_OK : S12_ERR_CUDA;
+    return encode([&](PFN_cuTensorMapEncodeTiled_v12000 enc) {
+        return enc(out, dtype, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle_mode(swizzle), CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 }  // namespace
 
 int make_tmap_u8_3d(CUtensorMap *out, const void *base, uint64_t inner, uint64_t d1, uint64_t d2, uint64_t stride1,
                     uint64_t stride2, uint32_t box_inner, uint32_t box1, uint32_t box2, int swizzle) {
-    auto enc = encoder();
-    if (!enc) return S12_ERR_CUDA;
     const cuuint64_t dims[3] = {inner, d1, d2};
     const cuuint64_t strides[2] = {stride1, stride2};
     const cuuint32_t box[3] = {box_inner, box1, box2};
     const cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_mode(swizzle), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? S12_OK : S12_ERR_CUDA;
+    return encode([&](PFN_cuTensorMapEncodeTiled_v12000 enc) {
+        return enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_mode(swizzle), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 }  // namespace s12
