@@ -794,7 +794,8 @@ int run_gemm(const s12_view *views, int count, const uint16_t *const *x, const i
     p.a_bufs = pl.a_bufs;
     p.tmem_cols = pl.tmem_cols;
     auto kern = gemm::gemm_tc_kernel<CHECK, NP, V>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem) != cudaSuccess)
+    // (always the same limit: another thread's call may be between this line and its launch)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
         return S12_ERR_CUDA;
     kern<<<pl.grid, gemm::kThreads, pl.smem, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? S12_OK : S12_ERR_CUDA;

@@ -700,7 +700,8 @@ int ranges_of(int rest, int workers, int chunks, uint32_t stage_bytes, int token
 template <int CG>
 int run8(const gemm8::Params &p, int workers, uint32_t smem, cudaStream_t stream) {
     auto kern = gemm8::gemm_i8_kernel<CG>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    // (always the same limit: another thread's call may be between this line and its launch)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
         return S12_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(workers * CG);

@@ -1829,7 +1829,8 @@ int launch_moe(const MoeCall &c, void *ws, size_t ws_bytes, cudaStream_t stream)
     const bool v1 = c.up->version == 1;
     auto kern = pl.small ? (v1 ? moe::moe_small_kernel<1> : moe::moe_small_kernel<2>)
                          : (v1 ? moe::moe_large_kernel<1> : moe::moe_large_kernel<2>);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem) != cudaSuccess)
+    // (always the same limit: another thread's call may be between this line and its launch)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
         return S12_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sms);
