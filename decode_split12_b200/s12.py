@@ -443,6 +443,22 @@ def _here(t: torch.Tensor | None, dev: int):
     return t.data_ptr()
 
 
+def _word(t: torch.Tensor | None, dev: int):
+    """The address of an error word: the kernels write four bytes there."""
+    if t is not None and t.numel() * t.element_size() < 4:
+        raise ValueError(f"err_flag: expected four bytes or more, got {t.numel()} of {t.dtype}")
+    return _here(t, dev)
+
+
+def _container(view: View, dev: int):
+    """A view whose container is memory of the current device (where the view
+    knows its container, as s12_open's do)."""
+    blob = getattr(view, "_blob", None)
+    if blob is not None and blob.get_device() != dev:
+        raise ValueError(f"expected a container on the current device (cuda:{dev}), got one on {blob.device}")
+    return C.byref(view)
+
+
 def _raw_stream(dev: int):
     """The current stream.  A call with a stream makes it the current one, so
     that what it allocates is cleared, written and given back on it."""
@@ -575,7 +591,7 @@ def s12_gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     dev = torch.cuda.current_device()
     rc = _lib().s12_gemm_i8(_here(x, dev), _here(x_scale, dev), _here(w, dev), _here(w_scale, dev), M, N, K,
                             _here(y, dev), _value_type(y), _here(ws, dev), ws.numel() * ws.element_size(),
-                            _here(err_flag, dev), _raw_stream(dev))
+                            _word(err_flag, dev), _raw_stream(dev))
     if rc:
         raise S12Error(rc, "s12_gemm_i8")
     return y
@@ -618,9 +634,9 @@ def s12_moe(gate_up: View, down: View, experts: int, x: torch.Tensor, router: to
     if ws is None:
         ws = moe_workspace(gate_up, down, experts, T, top_k, x.device)
     dev = torch.cuda.current_device()
-    rc = _lib().s12_moe(C.byref(gate_up), C.byref(down), experts, _here(x, dev), T, _here(router, dev), top_k,
+    rc = _lib().s12_moe(_container(gate_up, dev), _container(down, dev), experts, _here(x, dev), T, _here(router, dev), top_k,
                         int(renorm), _here(y, dev), _value_type(y), _here(ids, dev), _here(weights, dev),
-                        _here(ws, dev), ws.numel() * ws.element_size(), _here(err_flag, dev),
+                        _here(ws, dev), ws.numel() * ws.element_size(), _word(err_flag, dev),
                         _raw_stream(dev))
     if rc:
         raise S12Error(rc, "s12_moe")
@@ -645,9 +661,9 @@ def s12_moe_routed(gate_up: View, down: View, experts: int, x: torch.Tensor, ids
     if ws is None:
         ws = moe_workspace(gate_up, down, experts, T, top_k, x.device)
     dev = torch.cuda.current_device()
-    rc = _lib().s12_moe_routed(C.byref(gate_up), C.byref(down), experts, _here(x, dev), T, _here(ids, dev),
+    rc = _lib().s12_moe_routed(_container(gate_up, dev), _container(down, dev), experts, _here(x, dev), T, _here(ids, dev),
                                _here(weights, dev), top_k, _here(y, dev), _value_type(y), _here(ws, dev),
-                               ws.numel() * ws.element_size(), _here(err_flag, dev), _raw_stream(dev))
+                               ws.numel() * ws.element_size(), _word(err_flag, dev), _raw_stream(dev))
     if rc:
         raise S12Error(rc, "s12_moe_routed")
     return y
