@@ -697,6 +697,32 @@ int ranges_of(int rest, int workers, int chunks, uint32_t stage_bytes, int token
     return saved > 3000.0 + 20.0 * tokens * parts ? ranges : rest;
 }
 
+// Warps to a group of rows: the fewest columns' time.  The blocks go in waves of
+// two an SM, and a wave takes its warps' columns of a row and some 1300 more (it
+// starts, and its sums are reduced), whether it is full or not.  One token, us, by
+// 1, 2, 4 and 8 warps:
+//   900 x 4112    5.03  3.69  2.94  2.64 *     7000 x 12304  18.3 * 18.8   18.5   18.7
+//   1800 x 4112   5.44  4.12  3.37 * 4.67      7000 x 28016  36.7   37.6   35.6 * 34.8
+//   3500 x 4112   6.21  4.99 * 5.74  7.00      14000 x 1040   5.7 *  7.1   11.6   20.3
+//   3500 x 20000  20.3  15.0 * 17.1  16.3      14000 x 4112  14.2   14.0 * 15.6   23.8
+//   7000 x 4112   7.84 * 9.08  9.00  12.8      30000 x 4112  25.8 * 25.8   29.8   49.3
+//   7000 x 10000  14.8 * 16.3  16.5  17.0      30000 x 12304 66.5   62.7 * 63.1   66.8
+// (* is what is taken; over 138 sizes of 1 to 8 tokens it is within 4.5 % of the
+// best of the four, and 0.1 % on average).
+int dot_split(int64_t N, int64_t K, int sms) {
+    const int64_t groups = (N + gemm8::kDotRows - 1) / gemm8::kDotRows, warps = gemm8::kDotThreads / 32;
+    int best = 1;
+    int64_t least = 0;
+    for (int split = 1; split <= warps; split *= 2) {
+        const int64_t blocks = (groups * split + warps - 1) / warps, waves = (blocks + 2 * sms - 1) / (2 * sms);
+        const int64_t cost = waves * (K / split + 1300);
+        if (split > 1 && cost >= least) continue;
+        least = cost;
+        best = split;
+    }
+    return best;
+}
+
 template <int CG>
 int run8(const gemm8::Params &p, int workers, uint32_t smem, cudaStream_t stream) {
     auto kern = gemm8::gemm_i8_kernel<CG>;
@@ -754,13 +780,7 @@ int launch_gemm_i8(const Gemm8Call &c, void *ws, size_t ws_bytes, cudaStream_t s
     if (c.M <= 2 || (c.M <= kDotTokens && static_cast<unsigned long long>(c.M) * c.N * c.K <= 3ull << 26)) {
         gemm8::DotParams d = {c.x, c.w, c.x_scale, c.w_scale, c.y, c.N, c.y_type == S12_TYPE_F32,
                               static_cast<int>(c.M), static_cast<int>(c.K), 1};
-        // eight warps an SM and rows that are not too long for one (one token, us,
-        // by 1, 2, 4 and 8 warps a group of rows: 4096 x 14336 14.2 11.3 12.4 12.9;
-        // 14336 x 4096 12.1 12.5 14.6 23.3; 28672 x 8192 40.7 37.2 37.9 49.8;
-        // 1024 x 4096 3.7 2.7 2.2 2.1)
-        while (d.split < gemm8::kDotThreads / 32 &&
-               ((c.N + 3) / 4 * d.split < 8 * sms || c.K > 7168ll * d.split))
-            d.split *= 2;
+        d.split = dot_split(c.N, c.K, sms);
         if (c.M == 1) return run_dot<1>(d, stream);
         if (c.M == 2) return run_dot<2>(d, stream);
         if (c.M <= 4) return run_dot<4>(d, stream);
