@@ -14,8 +14,8 @@ copy bandwidth achieved on the compressed bytes actually moved.
                     [--no-cpu-baseline] [--no-gemm] [--no-decode] [--no-stack]
 
 The line's roofline.comparisons carry the uncompressed BF16 GEMV on the same
-layer, the 4096 x 4096 single tensor, the layer from version 2 containers
-and the encoder; `extra` the other batches, launch groupings, the SwiGLU
+layer, the layer in 8 bits, the 4096 x 4096 single tensor, the layer from
+version 2 containers and the encoder; `extra` the other batches, launch groupings, the SwiGLU
 epilogue, the skinny GEMM, the standalone decode, the 32-layer stack (also
 as an activation chain) and the MoE block.
 
@@ -575,6 +575,40 @@ def encode_llama(layer, world):
                       "packing), best of 3 per matrix"}
 
 
+def int8_layer(layer, world, steps: int, fused_us: float):
+    """The same seven matrices in 8 bits (s12_quant_i8 once, a scale per row),
+    the lossy form that lossless 12 bits are compared with: each x quantised
+    and multiplied by s12_gemm_i8, fourteen launches, against the fused GEMV
+    as seven.  The error is that of y against the fused GEMV's y, relative in
+    the root mean square over the layer."""
+    import torch
+
+    from decode_split12_b200 import s12
+    ws = s12.gemm_i8_workspace(layer.batch, device="cuda")
+    w = {n: s12.s12_quant_i8(layer.w_dev[n].view(torch.bfloat16)) for n in layer.names}
+    x = {n: layer.x[n].view(torch.bfloat16).reshape(layer.batch, -1) for n in layer.names}
+    xq = {n: s12.s12_quant_i8(x[n]) for n in layer.names}
+    y = {n: torch.empty_like(layer.y[n]) for n in layer.names}
+
+    def step():
+        for n in layer.names:
+            s12.s12_quant_i8(x[n], *xq[n])
+            s12.s12_gemm_i8(*xq[n], *w[n], y[n], ws)
+
+    g = capture(step)
+    for _ in range(3):
+        g.replay()
+    t = time_graph(g, steps, world) / steps
+    layer.step_separate()
+    torch.cuda.synchronize()
+    off = sum(float((y[n] - layer.y[n]).double().square().sum()) for n in layer.names)
+    size = sum(float(layer.y[n].double().square().sum()) for n in layer.names)
+    del g
+    return {"us_14_launches": round(t * 1e6, 2), "fused_us_7_launches": fused_us,
+            "weight_bytes": sum(q.numel() + 4 * c.numel() for q, c in w.values()),
+            "container_bytes": layer.compressed, "rel_rms_error_vs_fused": round(math.sqrt(off / size), 6)}
+
+
 def run_llama8b(args, world, rank):
     import torch
     hbm, _, _, peak_kind = load_peaks()
@@ -637,6 +671,8 @@ def run_llama8b(args, world, rank):
             "fused_us": round(ms * 1e3, 2), "bf16_own_gemv_us": extra["bf16_own_gemv"]["us_per_layer"],
             "cublas_bf16_us": extra["bf16_torch_linear"]["us_per_layer"],
             "fused_speedup_vs_faster_bf16": round(fast_bf16 / (ms * 1e3), 4)}
+        comparisons["int8_same_layer"] = int8_layer(layer, world, max(20, args.steps // 2),
+                                                    extra["separate_7_launches"]["us_per_layer"])
         comparisons["encode_llama8b_layer"] = encode_llama(layer, world)
     comparisons["container_v2_same_layer"] = v2_layer(layer, world, max(20, args.steps // 2))
     comparisons["single_4096_b1"] = single_c1(world)
