@@ -28,12 +28,12 @@
 // to arrive adds the others' to its own, scales and stores.  Integer sums do
 // not depend on their order.
 //
-// Measured (us; bytes against a measured copy's 6.53 TB/s, operations against 4.5
-// POP/s nominal): 1 token of 4096 x 14336 11.3 (0.79 of the bytes), of 28672 x 8192
-// 37 (0.97); 64 tokens of 28672 x 8192 47 (0.77); 256 tokens 61 (0.63; the
-// tensor cores' 27 us and the bytes' 39 do not quite overlap); 4096 tokens of
-// 14336 x 4096 170 (2.8 POP/s, 0.63 of the operations; cuBLAS's integer product
-// 158).
+// Measured (us in a graph, weights not in L2; bytes against a measured copy's 6.53
+// TB/s, operations against 4.5 POP/s nominal): 1 token of 4096 x 14336 12.0 (0.75 of
+// the bytes), of 28672 x 8192 39.7 (0.91); 19 tokens of 5000 x 2064 8.8; 64 of 28672 x
+// 8192 48.8 (0.75; cuBLAS's integer product 53.5); 256 tokens 61.0 (0.63; 58.0: the
+// tensor cores' 27 us and the bytes' 39 do not quite overlap); 4096 tokens of 14336 x
+// 4096 167 (2.9 POP/s, 0.64 of the operations; 155).
 #include <algorithm>
 
 #include <cuda_bf16.h>

@@ -38,17 +38,25 @@
 // bounded.  One that gives up raises S12_FLAG_TIMEOUT and a word that the other
 // waits watch; the CTAs then leave, and the last one clears the words.
 //
-// Measured (5e-4 of the weights far outside their tiles' window; us, and the
-// experts' compressed bytes against a measured copy's 6.53 TB/s):
-//   8 experts of 14336 x 4096, top 2:  1 token 143 (0.58), 2 tokens 193 (0.64),
-//     8 tokens 420 (0.69), 16 tokens 503 (0.66), 64 tokens 515 (0.64)
-//   32 experts of 1408 x 2176, top 4:  1 token 50, 9 tokens 130 (0.45), 64 187 (0.37)
-//   64 experts of 1024 x 2048, top 8:  1 token 55, 16 tokens 165 (0.51), 64 192 (0.50)
-// A call of one token begins and ends in about 25 us (the choice of experts,
-// three meetings of the grid at 1.3 us, the sums).  Beyond that the small kernel
-// waits for the instructions that decode and multiply, the large one for those
-// that put escapes right and read metadata (without either 465 of the 515 us,
-// without both 382).
+// Measured (5e-4 of the weights 10 to 100 times as large as the rest; us in a
+// graph, and the experts' compressed bytes against a measured copy's 6.53 TB/s):
+//   8 experts of 14336 x 4096, top 2:  1 token 149 (0.56), 2 tokens that meet 3
+//     experts 212 (0.59), 8 that meet 7 421 (0.69), 16 tokens 482 (0.69), 64 tokens
+//     507 (0.65; 489 with the pairs spread evenly, up to 554 where one expert has
+//     more than 40 of them)
+//   32 experts of 1408 x 2176, top 4:  1 token 53, 9 tokens that meet 21 to 24
+//     experts 113 to 128 (0.40), 64 193 (0.36)
+//   64 experts of 1024 x 2048, top 8:  1 token 57, 16 tokens 160 (0.49), 64 200 (0.47)
+// Copies of the kernels without a part (us; results wrong, timed only), for 64 tokens
+// and one token of the 8 experts:
+//   as they are 507, 150; escapes not put right 465, 128; no metadata read (and so
+//   no escapes) 470, 133; nothing decoded, nor put right 455, 120; neither 388, 116
+// So no part alone binds either kernel, and their schedulers issue in less than half
+// of the cycles: they wait.  A call of one token begins and ends in about 25 us (the
+// choice of experts, three meetings of the grid at 1.3 us, the sums).
+// Version 2 containers: 1 token 174, 64 tokens 758, 64 tokens of the 64 experts 218.
+// The counts of a row's earlier tiles are added up anew for every unit (a stage with
+// escapes, in the small kernel), which grows with the square of a row.
 #include <algorithm>
 #include <type_traits>
 
@@ -1044,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_small_kernel(const __grid_con
 // TMEM, where the threads that decode it write it from registers: a row of the
 // tile is a lane of TMEM.  (Through mma.sync, every warp reads all of x from
 // shared memory for 16 rows of weights: 64 tokens of 8 experts of 14336 x 4096
-// took 815 us, against 515.)  x and h are copied to shared memory as the product
+// took 815 us, against 507.)  x and h are copied to shared memory as the product
 // wants them (128-byte swizzle).  h's high and low parts are one product of twice
 // the width, whose halves are added where the sums are stored: a product takes as
 // long for 64 columns as for 32 (two in a row: 607 us, one: 573).
@@ -1140,7 +1148,7 @@ __device__ __forceinline__ bool lost(const Params &p, LargeShared *sm) {
 // are a multiple of 16); the rest are whatever shared memory holds, and their sums
 // are not read.  Stages are as long as the largest segment needs, and their number
 // tells: with h in eights, 33 to 40 pairs leave four stages instead of three (64
-// tokens: 525 us against 555).
+// tokens, one expert with 40 of the pairs: 509 us; with 41, and three stages, 554).
 template <int PH>
 __device__ __forceinline__ uint32_t product_pairs(uint32_t n) {
     constexpr uint32_t kUp = 16 / PH - 1;
@@ -1724,7 +1732,7 @@ MoePlan plan(const MoeCall &c) {
     // by the products' multiply-adds, which is what the mma.sync kernel is slow
     // at; the other one costs 10 to 20 us more to begin with.  Here and there, us:
     // 8 experts of 14336 x 4096, top 2: 4 tokens (1.4e9) 373 and 364, 8 tokens
-    // (2.8e9) 437 and 420, 64 tokens 1251 and 515; 32 of 1408 x 2176, top 4: 48
+    // (2.8e9) 437 and 420, 64 tokens 1251 and 507; 32 of 1408 x 2176, top 4: 48
     // tokens (1.8e9) 170 and 186, 64 tokens (2.4e9) 208 and 187; 64 of 1024 x
     // 2048, top 8: 16 tokens (0.8e9) 165 and 169, 64 tokens (3.2e9) 245 and 192
     pl.small = slots * 3 * H * F <= 1ull << 31;

@@ -357,7 +357,7 @@ int launch_kind(const norm::Args &a, int sms, cudaStream_t stream) {
         return launch_rows(warp_kernel<4, PLAIN>, grid, 32 * kWarpRows, a, stream);
     }
     // Few rows: as many threads as vectors, so that each loads once (one row of
-    // 4096: 2.5 us).  Many rows: four vectors a thread, so that more rows share
+    // 4096: 2.2 us).  Many rows: four vectors a thread, so that more rows share
     // an SM (4096 rows of 8192, norm and quantiser: 45 and 24 us, against 49
     // and 28 with two and 62 and 41 with one).
     const unsigned grid = static_cast<unsigned>(a.rows);

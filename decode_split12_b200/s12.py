@@ -634,8 +634,8 @@ def s12_moe(gate_up: View, down: View, experts: int, x: torch.Tensor, router: to
     if ws is None:
         ws = moe_workspace(gate_up, down, experts, T, top_k, x.device)
     dev = torch.cuda.current_device()
-    rc = _lib().s12_moe(_container(gate_up, dev), _container(down, dev), experts, _here(x, dev), T, _here(router, dev), top_k,
-                        int(renorm), _here(y, dev), _value_type(y), _here(ids, dev), _here(weights, dev),
+    rc = _lib().s12_moe(_container(gate_up, dev), _container(down, dev), experts, _here(x, dev), T,
+                        _here(router, dev), top_k, int(renorm), _here(y, dev), _value_type(y), _here(ids, dev), _here(weights, dev),
                         _here(ws, dev), ws.numel() * ws.element_size(), _word(err_flag, dev),
                         _raw_stream(dev))
     if rc:
